@@ -62,4 +62,45 @@ cudaError_t launch_stream_fence(cudaStream_t s);
 cudaError_t launch_gemm_tc(const qnt_desc& d, const void* codes, const void* meta, long z0, const void* X, void* Y,
                            int M, int xbf16, int* st, cudaStream_t s, bool* handled);
 
+// Page tables and slots (kv_slots.cu).
+struct KvSlotsArgs {
+  const int32_t *len, *add;
+  int32_t *table, *free;
+  const int32_t* free_count;
+  int32_t *len_out, *cu, *slots, *free_count_out;
+  int rows, width, tokens, page, pages;
+  int* status;
+};
+cudaError_t launch_kv_slots(const KvSlotsArgs& a, cudaStream_t s);
+
+// Quantizing write into the key/value cache (kv_append.cu); index 0: K, 1: V.
+struct KvAppendArgs {
+  uint8_t* codes[2];
+  float* scales[2];
+  const void* x[2];
+  int64_t stride;
+  const int32_t* slots;
+  int tokens, page, pages, heads;
+  int* status;
+};
+cudaError_t launch_kv_append(const qnt_kv_desc& d, const KvAppendArgs& a, int xbf16, cudaStream_t s);
+
+// Attention over the key/value cache (kv_attn.cu).
+struct KvAttnArgs {
+  const uint8_t *kcodes, *vcodes;
+  const float *kscales, *vscales;
+  const void* q;
+  void* y;
+  int64_t q_stride, y_stride;
+  const int32_t *cu, *len, *table;
+  void* work;
+  int* status;
+  int rows, width, tokens;
+  int heads, group;      // key/value heads, query heads of each
+  int page_log2, pages, window;
+  float scale_log2;      // scale * log2(e)
+};
+size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new);
+cudaError_t launch_kv_attn(const qnt_kv_desc& d, const KvAttnArgs& a, int max_new, int xbf16, cudaStream_t s);
+
 }  // namespace qnt

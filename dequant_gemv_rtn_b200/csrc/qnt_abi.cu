@@ -1,6 +1,7 @@
 // qnt_abi.cu -- the C ABI of libqnt: argument validation, buffer sizes and
 // kernel dispatch.  Nothing here allocates memory; every launch goes to the
 // caller's stream.
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -118,6 +119,7 @@ const char* qnt_strerror(int code) {
     case QNT_ERR_TIMEOUT: return "device: a bounded wait for an asynchronous copy expired";
     case QNT_ERR_NONFINITE: return "device: NaN or Inf in the weights";
     case QNT_ERR_RANGE: return "device: a scale or FP16 code overflowed fp16";
+    case QNT_ERR_PAGES: return "device: the free pages do not cover a request's new tokens";
     default: return "unknown error code";
   }
 }
@@ -227,6 +229,134 @@ int qnt_gemv(const qnt_desc* desc, const void* d_codes, const void* d_meta, cons
   if (!aligned16(d_codes) || !aligned16(d_x) || !aligned16(d_y) || (d_meta && !aligned16(d_meta))) return QNT_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_rc(dispatch_gemm(*desc, d_codes, d_meta, d_x, d_y, 1, xdtype == QNT_BF16, d_status, s));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ key/value cache
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_kv(const qnt_kv_desc* d) {
+  if (!d) return QNT_ERR_ARG;
+  if (d->fmt != QNT_KV_INT8 && d->fmt != QNT_KV_E4M3) return QNT_ERR_ARG;
+  if (d->page != 16 && d->page != 32 && d->page != 64 && d->page != 128) return QNT_ERR_SHAPE;
+  if (d->dim != 64 && d->dim != 128 && d->dim != 256) return QNT_ERR_SHAPE;
+  if (d->heads < 1 || d->heads > 1024) return QNT_ERR_SHAPE;
+  if (d->pages < 1 || (int64_t)d->pages * d->page > INT32_MAX) return QNT_ERR_SHAPE;
+  return QNT_OK;
+}
+
+// A batch of rows whose page tables are `width` wide.  Positions, and sums of two
+// of them, are ints.
+int check_rows(const qnt_kv_desc& d, int rows, int width, int tokens) {
+  if (rows < 1 || rows > QNT_KV_MAX_ROWS || tokens < 0 || tokens > QNT_KV_MAX_TOKENS) return QNT_ERR_SHAPE;
+  if (width < 1 || (int64_t)width * d.page > QNT_KV_MAX_TOKENS) return QNT_ERR_SHAPE;
+  return QNT_OK;
+}
+
+int check_stride(int64_t stride, int64_t row) { return stride < row || stride % 8 != 0 ? QNT_ERR_SHAPE : QNT_OK; }
+
+}  // namespace
+
+extern "C" {
+
+int qnt_check_kv_desc(const qnt_kv_desc* desc) { return check_kv(desc); }
+
+size_t qnt_kv_codes_bytes(const qnt_kv_desc* d) {
+  return check_kv(d) != QNT_OK ? 0 : (size_t)d->pages * d->heads * d->page * d->dim;
+}
+
+size_t qnt_kv_scales_bytes(const qnt_kv_desc* d) {
+  return check_kv(d) != QNT_OK ? 0 : (size_t)d->pages * d->heads * sizeof(float);
+}
+
+int qnt_kv_slots(const qnt_kv_desc* desc, const int32_t* d_len, const int32_t* d_add, int32_t* d_table, int32_t* d_free,
+                 const int32_t* d_free_count, int32_t* d_len_out, int32_t* d_cu, int32_t* d_slots,
+                 int32_t* d_free_count_out, int rows, int width, int tokens, int* d_status, void* stream) {
+  int e = check_kv(desc);
+  if (e == QNT_OK) e = check_rows(*desc, rows, width, tokens);
+  if (e != QNT_OK) return e;
+  const void* ptrs[] = {d_len, d_add, d_table, d_free, d_free_count, d_len_out, d_cu, d_free_count_out};
+  for (const void* p : ptrs)
+    if (!p) return QNT_ERR_ARG;
+  if (!d_slots && tokens > 0) return QNT_ERR_ARG;
+  // several CTAs read the inputs while others write: no output in an input's place
+  if (d_len_out == d_len || d_len_out == d_add || d_free_count_out == d_free_count) return QNT_ERR_ARG;
+  for (const void* p : ptrs)
+    if (!aligned4(p)) return QNT_ERR_ALIGN;
+  if (!aligned4(d_slots)) return QNT_ERR_ALIGN;
+  qnt::KvSlotsArgs a = {d_len, d_add, d_table, d_free, d_free_count, d_len_out, d_cu, d_slots, d_free_count_out,
+                        rows, width, tokens, desc->page, desc->pages, d_status};
+  return cuda_rc(qnt::launch_kv_slots(a, static_cast<cudaStream_t>(stream)));
+}
+
+int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float* d_kscales, float* d_vscales,
+                  const void* d_k, const void* d_v, int64_t stride, const int32_t* d_slots, int tokens, int xdtype,
+                  int* d_status, void* stream) {
+  int e = check_kv(desc);
+  if (e != QNT_OK) return e;
+  if (xdtype != QNT_F16 && xdtype != QNT_BF16) return QNT_ERR_ARG;
+  if (tokens < 0 || tokens > QNT_KV_MAX_TOKENS) return QNT_ERR_SHAPE;
+  if ((e = check_stride(stride, (int64_t)desc->heads * desc->dim)) != QNT_OK) return e;
+  if (tokens == 0) return QNT_OK;
+  if (!d_kcodes || !d_vcodes || !d_kscales || !d_vscales || !d_k || !d_v || !d_slots) return QNT_ERR_ARG;
+  if (!aligned16(d_kcodes) || !aligned16(d_vcodes) || !aligned16(d_k) || !aligned16(d_v) || !aligned4(d_kscales) ||
+      !aligned4(d_vscales) || !aligned4(d_slots))
+    return QNT_ERR_ALIGN;
+  qnt::KvAppendArgs a = {{static_cast<uint8_t*>(d_kcodes), static_cast<uint8_t*>(d_vcodes)}, {d_kscales, d_vscales},
+                         {d_k, d_v}, stride, d_slots, tokens, desc->page, desc->pages, desc->heads, d_status};
+  return cuda_rc(qnt::launch_kv_append(*desc, a, xdtype == QNT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qnt_kv_attn_work_bytes(const qnt_kv_desc* desc, int heads, int max_new) {
+  if (check_kv(desc) != QNT_OK || heads < 1 || heads % desc->heads != 0 || max_new < 1) return 0;
+  return qnt::kv_attn_work_bytes(*desc, heads, max_new);
+}
+
+int qnt_kv_attn(const qnt_kv_desc* desc, const void* d_kcodes, const void* d_vcodes, const float* d_kscales,
+                const float* d_vscales, const void* d_q, int64_t q_stride, void* d_y, int64_t y_stride, int heads,
+                const int32_t* d_cu, const int32_t* d_len, const int32_t* d_table, int rows, int width, int tokens,
+                int max_new, float scale, int window, void* d_work, int xdtype, int* d_status, void* stream) {
+  int e = check_kv(desc);
+  if (e == QNT_OK) e = check_rows(*desc, rows, width, tokens);
+  if (e != QNT_OK) return e;
+  if (xdtype != QNT_F16 && xdtype != QNT_BF16) return QNT_ERR_ARG;
+  if (heads < 1 || heads > 65536 || heads % desc->heads != 0) return QNT_ERR_SHAPE;
+  if (max_new < 1 || window < 0 || !(scale > -INFINITY && scale < INFINITY)) return QNT_ERR_ARG;
+  const int64_t row = (int64_t)heads * desc->dim;
+  if ((e = check_stride(q_stride, row)) != QNT_OK || (e = check_stride(y_stride, row)) != QNT_OK) return e;
+  if (tokens == 0) return QNT_OK;
+  if (!d_kcodes || !d_vcodes || !d_kscales || !d_vscales || !d_q || !d_y || !d_cu || !d_len || !d_table || !d_work)
+    return QNT_ERR_ARG;
+  if (!aligned16(d_kcodes) || !aligned16(d_vcodes) || !aligned16(d_q) || !aligned16(d_y) || !aligned16(d_work) ||
+      !aligned4(d_kscales) || !aligned4(d_vscales) || !aligned4(d_cu) || !aligned4(d_len) || !aligned4(d_table))
+    return QNT_ERR_ALIGN;
+  qnt::KvAttnArgs a = {};
+  a.kcodes = static_cast<const uint8_t*>(d_kcodes);
+  a.vcodes = static_cast<const uint8_t*>(d_vcodes);
+  a.kscales = d_kscales;
+  a.vscales = d_vscales;
+  a.q = d_q;
+  a.y = d_y;
+  a.q_stride = q_stride;
+  a.y_stride = y_stride;
+  a.cu = d_cu;
+  a.len = d_len;
+  a.table = d_table;
+  a.work = d_work;
+  a.status = d_status;
+  a.rows = rows;
+  a.width = width;
+  a.tokens = tokens;
+  a.heads = desc->heads;
+  a.group = heads / desc->heads;
+  a.page_log2 = desc->page == 16 ? 4 : desc->page == 32 ? 5 : desc->page == 64 ? 6 : 7;
+  a.pages = desc->pages;
+  a.window = window < width * desc->page ? window : 0;   // a longer one hides nothing
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return cuda_rc(qnt::launch_kv_attn(*desc, a, max_new, xdtype == QNT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

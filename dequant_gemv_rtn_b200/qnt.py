@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libqnt.so")
 QNT_INT4_ASYM, QNT_FP4_E2M1, QNT_FP4_AFPQ, QNT_FP4_RAZER, QNT_INT8_PERCHAN, QNT_FP16 = 1, 2, 3, 4, 5, 6
 QNT_F16, QNT_BF16 = 0, 1
 (QNT_OK, QNT_ERR_ARG, QNT_ERR_SHAPE, QNT_ERR_ALIGN, QNT_ERR_CUDA, QNT_ERR_TIMEOUT,
- QNT_ERR_NONFINITE, QNT_ERR_RANGE) = range(8)
+ QNT_ERR_NONFINITE, QNT_ERR_RANGE, QNT_ERR_PAGES) = range(9)
 FORMATS = {"int4": QNT_INT4_ASYM, "fp4": QNT_FP4_E2M1, "afpq": QNT_FP4_AFPQ, "razer": QNT_FP4_RAZER,
            "int8": QNT_INT8_PERCHAN, "fp16": QNT_FP16}
 
@@ -25,6 +25,9 @@ FORMATS = {"int4": QNT_INT4_ASYM, "fp4": QNT_FP4_E2M1, "afpq": QNT_FP4_AFPQ, "ra
 QNT_MAX_GEMV_K = 32768
 QNT_SEQ_MAX_STEPS = 256
 QNT_SEQ_NOALLOC_MAX_STEPS = 256
+QNT_KV_INT8, QNT_KV_E4M3 = 1, 2
+QNT_KV_MAX_ROWS = 4096
+QNT_KV_MAX_TOKENS = 1 << 30
 
 
 class qnt_desc(ctypes.Structure):
@@ -36,12 +39,18 @@ class qnt_seq_step(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("wait", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class qnt_kv_desc(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("page", ctypes.c_int32), ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"libqnt.so not found at {LIB_PATH}; run `python -m dequant_gemv_rtn_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     D = ctypes.POINTER(qnt_desc)
+    KD, L, F = ctypes.POINTER(qnt_kv_desc), ctypes.c_int64, ctypes.c_float
     sig = {
         "qnt_version": (I, []),
         "qnt_check_desc": (I, [D]),
@@ -53,6 +62,13 @@ def _load():
         "qnt_gemv_seq_work_bytes": (Z, [I]),
         "qnt_gemv_seq": (I, [ctypes.POINTER(qnt_seq_step), I, I, P, P, P]),
         "qnt_gemv_seq_noalloc": (I, [ctypes.POINTER(qnt_seq_step), I, I, P, P]),
+        "qnt_check_kv_desc": (I, [KD]),
+        "qnt_kv_codes_bytes": (Z, [KD]),
+        "qnt_kv_scales_bytes": (Z, [KD]),
+        "qnt_kv_slots": (I, [KD, P, P, P, P, P, P, P, P, P, I, I, I, P, P]),
+        "qnt_kv_append": (I, [KD, P, P, P, P, P, P, L, P, I, I, P, P]),
+        "qnt_kv_attn_work_bytes": (Z, [KD, I, I]),
+        "qnt_kv_attn": (I, [KD, P, P, P, P, P, L, P, L, I, P, P, P, I, I, I, I, F, I, P, I, P, P]),
         "qnt_table_create": (P, [I, I]),
         "qnt_table_set": (I, [P, ctypes.c_char_p, I, I]),
         "qnt_table_lookup": (I, [P, ctypes.c_char_p, ctypes.POINTER(I), ctypes.POINTER(I)]),
@@ -173,6 +189,50 @@ def qnt_gemv_seq_noalloc(steps, xdtype: int, status=None, stream=None, check=Tru
     """qnt_gemv_seq without a caller workspace (the library's own counters)."""
     rc = lib.qnt_gemv_seq_noalloc(steps, len(steps), int(xdtype), _ptr(status), _stream(stream))
     return _check(rc, "qnt_gemv_seq_noalloc") if check else rc
+
+
+def kv_desc(fmt: int, page: int, pages: int, heads: int, dim: int) -> qnt_kv_desc:
+    return qnt_kv_desc(int(fmt), int(page), int(pages), int(heads), int(dim))
+
+
+def qnt_check_kv_desc(d: qnt_kv_desc) -> int:
+    return lib.qnt_check_kv_desc(ctypes.byref(d))
+
+
+def qnt_kv_codes_bytes(d: qnt_kv_desc) -> int:
+    return lib.qnt_kv_codes_bytes(ctypes.byref(d))
+
+
+def qnt_kv_scales_bytes(d: qnt_kv_desc) -> int:
+    return lib.qnt_kv_scales_bytes(ctypes.byref(d))
+
+
+def qnt_kv_slots(d: qnt_kv_desc, length, add, table, free, free_count, len_out, cu, slots, free_count_out, rows: int,
+                 width: int, tokens: int, status=None, stream=None, check=True) -> int:
+    rc = lib.qnt_kv_slots(ctypes.byref(d), _ptr(length), _ptr(add), _ptr(table), _ptr(free), _ptr(free_count),
+                          _ptr(len_out), _ptr(cu), _ptr(slots), _ptr(free_count_out), rows, width, tokens, _ptr(status),
+                          _stream(stream))
+    return _check(rc, "qnt_kv_slots") if check else rc
+
+
+def qnt_kv_append(d: qnt_kv_desc, k_codes, v_codes, k_scales, v_scales, k, v, stride: int, slots, tokens: int,
+                  xdtype: int = QNT_F16, status=None, stream=None, check=True) -> int:
+    rc = lib.qnt_kv_append(ctypes.byref(d), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(k), _ptr(v),
+                           stride, _ptr(slots), tokens, xdtype, _ptr(status), _stream(stream))
+    return _check(rc, "qnt_kv_append") if check else rc
+
+
+def qnt_kv_attn_work_bytes(d: qnt_kv_desc, heads: int, max_new: int = 1) -> int:
+    return lib.qnt_kv_attn_work_bytes(ctypes.byref(d), int(heads), int(max_new))
+
+
+def qnt_kv_attn(d: qnt_kv_desc, k_codes, v_codes, k_scales, v_scales, q, q_stride: int, y, y_stride: int, heads: int, cu,
+                length, table, rows: int, width: int, tokens: int, max_new: int, scale: float, window: int, work,
+                xdtype: int = QNT_F16, status=None, stream=None, check=True) -> int:
+    rc = lib.qnt_kv_attn(ctypes.byref(d), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(q), q_stride,
+                         _ptr(y), y_stride, heads, _ptr(cu), _ptr(length), _ptr(table), rows, width, tokens, max_new, scale,
+                         window, _ptr(work), xdtype, _ptr(status), _stream(stream))
+    return _check(rc, "qnt_kv_attn") if check else rc
 
 
 class qnt_table:

@@ -103,7 +103,8 @@ enum {
   QNT_ERR_CUDA = 4,      /* the kernel launch failed */
   QNT_ERR_TIMEOUT = 5,   /* (device) a bounded wait for an asynchronous copy expired */
   QNT_ERR_NONFINITE = 6, /* (device) NaN or Inf in W; codes are unspecified */
-  QNT_ERR_RANGE = 7      /* (device) a scale or FP16 code overflowed fp16 */
+  QNT_ERR_RANGE = 7,     /* (device) a scale or FP16 code overflowed fp16 */
+  QNT_ERR_PAGES = 8      /* (device) the free pages do not cover a request's new tokens */
 };
 
 /* Shape and format of one quantized matrix. */
@@ -284,6 +285,139 @@ int qnt_gemv_seq(const qnt_seq_step* steps, int nsteps, int xdtype, void* d_work
  */
 #define QNT_SEQ_NOALLOC_MAX_STEPS 256
 int qnt_gemv_seq_noalloc(const qnt_seq_step* steps, int nsteps, int xdtype, int* d_status, void* stream);
+
+/*
+ * Paged 8-bit key/value cache: what a decode step keeps of its past between the
+ * qkv and the o product.  ("The Power of Negative Zero: RaZeR", English
+ * abstract: quantization extends from the weights to the key/value cache; the
+ * pages give no formulas, so the arithmetic is the plain RTN one stated here.)
+ * Three calls make a step: qnt_kv_slots gives the step's new tokens their
+ * places, qnt_kv_append quantizes their keys and values into them, qnt_kv_attn
+ * lets their queries attend to the cache.
+ *
+ * A page holds `page` consecutive tokens of one request for every head.  K and
+ * V have a codes buffer and a scales buffer each:
+ *   codes  uint8 [pages][heads][page][dim]      scales  fp32 [pages][heads]
+ * so a scale serves the `page` tokens of a head in a page, and a value is
+ * code value * scale.  INT8 byte = q + 128 with q in -127..127 (zero-extended
+ * bytes are fp16 subnormals, the operand of the tensor cores); E4M3 byte =
+ * the OCP 8-bit float (sign, 4 exponent, 3 mantissa bits, largest value 448).
+ * A token's slot is page * (tokens in a page) + its place in the page.
+ */
+typedef enum { QNT_KV_INT8 = 1, QNT_KV_E4M3 = 2 } qnt_kv_fmt;
+
+#define QNT_KV_MAX_ROWS 4096             /* requests in one call */
+#define QNT_KV_MAX_TOKENS (1 << 30)      /* token rows in one call, and tokens of a page table (width * page) */
+
+typedef struct {
+  int32_t fmt;     /* qnt_kv_fmt */
+  int32_t page;    /* tokens in a page: 16, 32, 64 or 128 */
+  int32_t pages;   /* pages in the cache, >= 1; pages * page < 2^31 */
+  int32_t heads;   /* key/value heads, 1..1024 */
+  int32_t dim;     /* values in a head: 64, 128 or 256 */
+} qnt_kv_desc;
+
+/* Bytes of the codes buffer (and as many again for V) and of the scales buffer
+ * (likewise); 0 if the descriptor is invalid. */
+size_t qnt_kv_codes_bytes(const qnt_kv_desc* desc);
+size_t qnt_kv_scales_bytes(const qnt_kv_desc* desc);
+
+/* QNT_OK or the error code that the calls would return. */
+int qnt_check_kv_desc(const qnt_kv_desc* desc);
+
+/*
+ * qnt_kv_slots -- page tables and slots of a step's new tokens (reads page and
+ * pages of the descriptor).  All arrays are device int32.
+ *   d_len      [rows] tokens that each request has cached, 0 for a new one.
+ *   d_add      [rows] new tokens of each request (0: none); -1 releases the
+ *              request's pages.
+ *   d_table    [rows][width] page of each `page` tokens of a request; entries of
+ *              cached tokens are read, those of new pages written, the others left.
+ *   d_free     [pages] a stack, its first *d_free_count entries the free pages.
+ *   d_len_out  [rows] written: d_len + d_add; 0 for a released request; d_len
+ *              for one that got no room.
+ *   d_cu       [rows + 1] written: first token row of each request (the requests'
+ *              new tokens one after another), at most `tokens`.
+ *   d_slots    [tokens] written: slot of each token row; -1 for the tokens of a
+ *              request that got no room and for the rows behind the last token.
+ *   d_free_count_out  [1] written.
+ * First every released request's pages go onto the stack (requests in order,
+ * pages in order), then the requests take new pages from its top, in order.
+ * The inputs d_len, d_add and d_free_count are not written, entries of d_free
+ * below *d_free_count neither, and no output may overlap an input, so a
+ * repeated call gives the same outputs.  Requests get no room, and the others
+ * are served, (a) from the first one on that the stack does not cover
+ * (QNT_ERR_PAGES; those that need no new page are served all the same), (b) when
+ * they would pass width * page tokens or their token rows `tokens`, or when
+ * d_len is outside 0..width * page (QNT_ERR_ARG in *d_status).  A page number of
+ * the free stack is trusted here and checked where it is used.
+ * 1 <= rows <= QNT_KV_MAX_ROWS, 1 <= width, width * page and tokens at most
+ * QNT_KV_MAX_TOKENS, else QNT_ERR_SHAPE (here and below).
+ */
+int qnt_kv_slots(const qnt_kv_desc* desc, const int32_t* d_len, const int32_t* d_add, int32_t* d_table, int32_t* d_free,
+                 const int32_t* d_free_count, int32_t* d_len_out, int32_t* d_cu, int32_t* d_slots,
+                 int32_t* d_free_count_out, int rows, int width, int tokens, int* d_status, void* stream);
+
+/*
+ * qnt_kv_append -- quantizes the keys and values of token rows into their slots.
+ *   d_kcodes, d_vcodes, d_kscales, d_vscales  the cache, updated.
+ *   d_k, d_v   device, [tokens] rows of heads * dim fp16 or bf16 (xdtype), rows
+ *              `stride` elements apart (a multiple of 8, >= heads * dim): slices
+ *              of the qkv product's output will do.
+ *   d_slots    device int32 [tokens], as from qnt_kv_slots; rows with a negative
+ *              slot are skipped.
+ * Token rows with consecutive slots of one page are a run.  For every run, head
+ * and of K and V: a = max |x| over the run, s = fp32(a / 127) (E4M3: a / 448); a
+ * run that does not begin its page keeps the page's scale if that is larger.
+ * The codes are the code values nearest to x / s (the real quotient, ties to
+ * even; 0 if s = 0).  If the scale of a page grows from s0 to s, the codes of
+ * the tokens before the run become those nearest to (code value * s0) / s.  The
+ * page's tokens behind the run are left as they are; their values are
+ * unspecified until they are written.  A page must not take part in two runs of
+ * one call: where a second one follows the first with nothing or only skipped
+ * rows in between it is not written (QNT_ERR_ARG in *d_status); elsewhere the
+ * page's content is unspecified.  A slot beyond the cache is
+ * skipped (QNT_ERR_ARG).  Non-finite x: QNT_ERR_NONFINITE, the scale is that of
+ * the finite values and the codes of the others are finite but unspecified.
+ * tokens = 0 does nothing.  Bit-exact with the definition.
+ */
+int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float* d_kscales, float* d_vscales,
+                  const void* d_k, const void* d_v, int64_t stride, const int32_t* d_slots, int tokens, int xdtype,
+                  int* d_status, void* stream);
+
+/*
+ * qnt_kv_attn -- attention of the new tokens over the cache.  Query head h uses
+ * key/value head h / (heads / desc->heads).  Token t of the n = d_cu[b+1] -
+ * d_cu[b] new tokens of request b has position p = d_len[b] - n + t and sees the
+ * cached tokens j <= p, with window > 0 only j > p - window:
+ *   y = sum_j softmax_j(scale * q . k_j) v_j        (0 if it sees none)
+ *   d_q        device, [tokens] rows of heads * dim fp16 or bf16 (xdtype), rows
+ *              q_stride elements apart (a multiple of 8, >= heads * dim).
+ *   d_y        device, the same with y_stride, written in the same type for the
+ *              token rows of requests; other rows are left as they are.
+ *   heads      query heads, a multiple of desc->heads.
+ *   d_cu       device int32 [rows + 1] as from qnt_kv_slots.
+ *   d_len      device int32 [rows], cached tokens with the new ones among them
+ *              (qnt_kv_slots' d_len_out).
+ *   d_table    device int32 [rows][width].
+ *   max_new    the largest n as far as the caller knows it (>= 1): it chooses the
+ *              kernel, not the result.
+ *   d_work     device, qnt_kv_attn_work_bytes bytes, 16-byte aligned, zeroed by
+ *              the caller before its first use; every call leaves it ready for
+ *              the next.  Two calls that may run at the same time need two.
+ * Products are of exact fp16 operands with fp32 accumulation (q is rescaled by a
+ * power of two per row where it is bf16), the softmax is fp32, its weights are
+ * rounded to fp16 for the second product, relative to a running maximum, and y
+ * once to its type.  The bytes of tokens that no query sees may be anything; a
+ * visible E4M3 byte must not be 0x7F or 0xFF (NaN; qnt_kv_append writes none).
+ * A page number outside the cache is read as page 0, and d_len beyond
+ * width * page is cut there (QNT_ERR_ARG in *d_status).
+ */
+size_t qnt_kv_attn_work_bytes(const qnt_kv_desc* desc, int heads, int max_new);   /* 0 on bad arguments */
+int qnt_kv_attn(const qnt_kv_desc* desc, const void* d_kcodes, const void* d_vcodes, const float* d_kscales,
+                const float* d_vscales, const void* d_q, int64_t q_stride, void* d_y, int64_t y_stride, int heads,
+                const int32_t* d_cu, const int32_t* d_len, const int32_t* d_table, int rows, int width, int tokens,
+                int max_new, float scale, int window, void* d_work, int xdtype, int* d_status, void* stream);
 
 /*
  * Selective precision (RTN page: raise the precision format of chosen layers
