@@ -1,34 +1,45 @@
 // kv_append.cu -- quantizes new keys and values into the paged 8-bit cache
 // (qnt_kv_append; layout and definition in include/qnt.h).
 //
-// A run (the new tokens of one page) shares a scale per head, s = max |x| / top,
-// so a run is one unit of work: read it once into registers, reduce max |x|,
-// write the codes.  The grid is (windows of eight token rows) x heads x {K, V},
-// a warp per token row: the warp whose row begins a run takes it when it has at
-// most eight tokens (a decode step's, a draft's); a longer one, of which a
-// window can begin only one, is shared by the CTA's eight warps, up to 16
-// tokens each.  A run that goes on in a page begun before keeps the page's
-// scale or raises it; raising it re-rounds the codes of the tokens before it.
-// That is a map of 256 bytes to 256 bytes, so it is tabulated in 64 bits (8
-// entries a lane) and applied by the whole CTA with table look-ups.
+// A run (the new tokens of one page) shares a scale per head, s = max |x| / top.
+// The grid is (windows of token rows) x heads x {K, V}; a lane holds eight values of
+// a token, a warp IT rounds of 256 / dim tokens.  Which rows form runs is only
+// known from the slots, so the rows' values are requested first, by row number,
+// and the slots are read beside them: two waits for memory, not four.  Rows that
+// do not go on from the row before are bits of a mask; a row's run is what lies
+// between two bits.  max |x| goes from the values to the run's entry in shared
+// memory by atomicMax on the (non-negative) float's bits, which does not depend
+// on the order.  A run that crosses the window's ends is completed by reading its
+// other rows, too (up to a page at either end, from L2); every window writes the
+// codes of its own rows, the one with the run's first row the scale.  (Another
+// may read the page's old scale before or after that: max(new, old) is the same.)
+//
+// A run that goes on in a page begun before keeps the page's scale or raises it;
+// raising re-rounds the codes of the tokens before it.  That is a map of 256
+// bytes to 256 bytes: a warp tabulates it in 64 bits and applies it by look-up.
 //
 // Rounding to the nearest code of the real quotient x / s without a division:
 // t = x * (1 / s) is off by at most two units in the last place, so only a t
-// next to a tie can round wrongly.  INT8: with q = rint(t), d = x - q s is exact
-// in fp32 (q s has 31 bits, the difference cancels to at most 24), so comparing
-// d with s / 2 decides.  E4M3: ties have at most five significant bits, so a t
-// whose 19 low bits are within four of zero goes through a 64-bit quotient
-// (exact enough: two products of 11 and 29 bits that differ, differ by 2^-33).
+// next to a tie can round wrongly, which a remainder then decides; what is not
+// finite or too small for 1 / s goes through a 64-bit quotient.  INT8: adding
+// 1.5 2^23 + 128 leaves q + 128 in the low byte, and |t - q| tells how near a tie
+// is.  E4M3: ties have five significant bits from 2^-6 on, so t is near one only if
+// its 20 low bits are within four of 2^19; below 2^-6, fewer than five.  (In one
+// page of seven a is a multiple of 7, and then 2 % of all x / s are ties: with the
+// 64-bit quotient for these, too, 8192 prompt tokens took 52 us.)
+//
 // Bound by memory for prompts (2 bytes read and 1 written per value), by latency
-// for a decode step (slots, then x and the scale, then the codes).
+// for a decode step.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace qnt {
 namespace {
 
-constexpr int kApWarps = 8;            // token rows of a window, warps of a CTA
-constexpr int kApShort = 8;            // longest run that one warp takes
+constexpr int kApWarps = 8;
+constexpr int kApThreads = 32 * kApWarps;
+constexpr int kApHalo = 128;                 // rows kept on either side of the window: a page
+constexpr int kApBad = 0x7FFFFFFF;           // a slot beyond the cache
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -40,264 +51,386 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
   return h2f(h & 0xFFFFu);
 }
-// y rounded towards zero, its last bit set if that was inexact: any later
-// rounding to 22 bits or fewer is then that of y.
-__device__ __forceinline__ float to_odd(double y) {
-  const float t = __double2float_rz(y);
-  return (double)t != y ? __uint_as_float(__float_as_uint(t) | 1u) : t;
+// Code byte nearest to y.  E4M3: y rounded towards zero with the last bit set if
+// that was inexact; any later rounding to 22 bits or fewer is then that of y.
+template <int FMT>
+__device__ __forceinline__ uint32_t nearest_byte(double y) {
+  if (FMT == QNT_KV_INT8) return (uint32_t)((int)fmin(fmax(rint(y), -127.0), 127.0) + 128);
+  float t = __double2float_rz(y);
+  if ((double)t != y) t = __uint_as_float(__float_as_uint(t) | 1u);
+  return e4m3x2(t, 0.0f) & 0xFFu;
 }
-
-// x / s -> code byte, x and s scaled alike by a power of two, inv = 1 / s.
-__device__ __forceinline__ uint32_t int8_byte(float x, float s, float inv, float half) {
-  float q = rintf(x * inv);
-  const float d = fmaf(-q, s, x);
-  const bool odd = ((int)q & 1) != 0;
-  if (d > half || (d == half && odd)) q += 1.0f;
-  else if (d < -half || (d == -half && odd)) q -= 1.0f;
-  return (uint32_t)((int)fminf(fmaxf(q, -127.0f), 127.0f) + 128);
-}
-__device__ __forceinline__ float e4m3_quotient(float x, float s, float inv) {
-  float t = x * inv;
-  if (((__float_as_uint(t) + 4u) & 0x7FFFFu) < 9u && t != 0.0f) t = to_odd((double)x / (double)s);
-  return t;
-}
-
 template <int FMT>
 __device__ __forceinline__ uint32_t requant_byte(uint32_t b, double s0, double s) {
-  if (FMT == QNT_KV_INT8) {
-    const double q = rint((double)((int)b - 128) * s0 / s);
-    return (uint32_t)((int)q + 128);
-  }
-  return e4m3x2(to_odd((double)e4m3_value(b) * s0 / s), 0.0f) & 0xFFu;
+  const double v = FMT == QNT_KV_INT8 ? (double)((int)b - 128) : (double)e4m3_value(b);
+  return nearest_byte<FMT>(v * s0 / s);
 }
 
-// A run or a warp's share of one: tokens t, t + step, ... of the rows
-// [t, end), IT rounds of TPL tokens; a lane holds eight values of a token.
-template <bool BF16, int D, int IT>
-struct Share {
-  static constexpr int LPT = D / 8;            // lanes of a token
-  uint4 v[IT];
-  float top;
-  bool bad;
-  __device__ __forceinline__ void load(const uint16_t* x, int64_t stride, int t, int end, int step, int lane) {
+template <bool BF16>
+__device__ __forceinline__ float2 value_pair(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return make_float2(h2f(w & 0xFFFFu), h2f(w >> 16));
+}
+// The eight codes of v in 64 bits (rare).
+template <int FMT, bool BF16>
+__device__ __noinline__ uint2 codes_exact(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[2] = {0, 0};
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    const float2 p = value_pair<BF16>(w[j >> 1]);
+    float x = j & 1 ? p.y : p.x;
+    if (!(x == x)) x = 0.0f;                                 // the cache holds no NaN
+    o[j >> 2] |= (s > 0.0f ? nearest_byte<FMT>((double)x / (double)s) : FMT == QNT_KV_INT8 ? 128u : 0u) << (8 * (j & 3));
+  }
+  return make_uint2(o[0], o[1]);
+}
+// max(|a|, b), NaN if either is
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float d;
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmax.NaN.f32 %0, t, %2;\n\t}" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// The same with t = x * inv next to a tie somewhere: the sign of a remainder,
+// rounded once, decides.  INT8: x - q s against s / 2 (exact: q s has 31 bits, the
+// difference cancels to 24).  E4M3: t is moved off the five-bit number m that it
+// is next to, to the side that x - m s tells.
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint2 codes_near(uint4 v, float s, float inv) {
+  if (FMT == QNT_KV_E4M3 && s == 0.0f) return make_uint2(0, 0);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[8];
+  bool nan = false;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int tok = t + i * step + lane / LPT;
-      v[i] = tok < end ? ldg_cg128(x + (int64_t)tok * stride + 8 * (lane % LPT)) : make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < 8; ++j) {
+    const float2 p = value_pair<BF16>(w[j >> 1]);
+    const float x = j & 1 ? p.y : p.x;
+    const float t = x * inv;
+    nan |= !(fabsf(t) < 1e30f);
+    if (FMT == QNT_KV_INT8) {
+      float q = rintf(t);
+      const float d = fmaf(-q, s, x), half = 0.5f * s;
+      const bool odd = ((int)q & 1) != 0;
+      q += (d > half || (d == half && odd) ? 1.0f : 0.0f) - (d < -half || (d == -half && odd) ? 1.0f : 0.0f);
+      c[j] = (uint32_t)((int)fminf(fmaxf(q, -127.0f), 127.0f) + 128);
+    } else {
+      const uint32_t b = __float_as_uint(t), m = (b + 4u) & ~0x7FFFFu;
+      const float r = fmaf(-__uint_as_float(m), s, x);
+      const uint32_t to = r == 0.0f ? m : (r > 0.0f) == (t > 0.0f) ? m + 1u : m - 1u;
+      c[j] = ((b + 4u) & 0x7FFFFu) < 9u ? to : b;
     }
   }
-  static __device__ __forceinline__ float2 pair(uint32_t w) {
-    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return make_float2(h2f(w & 0xFFFFu), h2f(w >> 16));
-  }
-  // max |x| of the finite values, over the warp
-  __device__ __forceinline__ void reduce() {
-    top = 0.0f;
-    bad = false;
+  if (nan) return codes_exact<FMT, BF16>(v, s);
+  if (FMT == QNT_KV_INT8)
+    return make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+  for (int j = 0; j < 4; ++j) c[j] = e4m3x2(__uint_as_float(c[2 * j]), __uint_as_float(c[2 * j + 1]));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+// The eight codes of v; inv = 1 / s, 0 for s = 0, NaN where that is out of range.
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint2 codes_of(uint4 v, float s, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[2];
+  bool sure;
+  if (FMT == QNT_KV_INT8) {
+    constexpr float kMagic = 12582912.0f + 128.0f;
+    uint32_t b[8];
+    float off = 0.0f;                          // the largest distance from a whole number
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = pair(w[j]);
-        const float a = fabsf(p.x), b = fabsf(p.y);
-        const bool fa = a < __int_as_float(0x7F800000), fb = b < __int_as_float(0x7F800000);
-        bad |= !fa || !fb;
-        top = fmaxf(top, fmaxf(fa ? a : 0.0f, fb ? b : 0.0f));
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = value_pair<BF16>(w[j]);
+      const float tx = p.x * inv, ty = p.y * inv;
+      const float rx = tx + kMagic, ry = ty + kMagic;
+      off = max_abs_nan(tx - (rx - kMagic), off);
+      off = max_abs_nan(ty - (ry - kMagic), off);
+      b[2 * j] = __float_as_uint(rx);
+      b[2 * j + 1] = __float_as_uint(ry);
     }
+    sure = off < 0.4999f;                      // false for NaN
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  // codes of the tokens: `out` is the run's first token's place, row0 its token row
-  template <int FMT>
-  __device__ __forceinline__ void store(uint8_t* out, int row0, float s, int t, int end, int step, int lane) const {
-    // scales below 2^-100 are scaled up, with x, so that 1 / s and the remainders stay normal
-    const float up = s < 7.888609e-31f ? 1.2089258e24f : 1.0f;
-    const float su = s * up, inv = s > 0.0f ? 1.0f / su : 0.0f, half = 0.5f * su;
+    for (int j = 0; j < 2; ++j)
+      o[j] = prmt(prmt(b[4 * j], b[4 * j + 1], 0x0040u), prmt(b[4 * j + 2], b[4 * j + 3], 0x0040u), 0x5410u);
+  } else {
+    uint32_t near = 0xFFFFFFFFu, c[4];         // the least of (20 low bits - 2^19 + 4) << 12: ties of 2^-6 and above
+    float all = 0.0f, least = 1.0f;                        // smaller ones have their ties elsewhere
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int tok = t + i * step + lane / LPT;
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t o[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 p = pair(w[j]);
-        p.x *= up;
-        p.y *= up;
-        uint32_t b;
-        if (FMT == QNT_KV_INT8) {
-          b = s > 0.0f ? int8_byte(p.x, su, inv, half) | (int8_byte(p.y, su, inv, half) << 8) : 0x8080u;
-        } else {
-          // a NaN quotient (x not finite, or s = 0) becomes 0: the cache holds no NaN
-          const float qx = s > 0.0f ? e4m3_quotient(p.x, su, inv) : 0.0f, qy = s > 0.0f ? e4m3_quotient(p.y, su, inv) : 0.0f;
-          b = e4m3x2(qx == qx ? qx : 0.0f, qy == qy ? qy : 0.0f);
-        }
-        o[j >> 1] |= b << (16 * (j & 1));
-      }
-      if (tok < end) *reinterpret_cast<uint2*>(out + (int64_t)(tok - row0) * D + 8 * (lane % LPT)) = make_uint2(o[0], o[1]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = value_pair<BF16>(w[j]);
+      const float tx = p.x * inv, ty = p.y * inv;
+      near = min(near, min(__float_as_uint(tx) * 4096u + 0x80004000u, __float_as_uint(ty) * 4096u + 0x80004000u));
+      least = fminf(least, fminf(fabsf(tx), fabsf(ty)));
+      all = fmaf(tx, 0.0f, fmaf(ty, 0.0f, all));   // NaN if one is not finite
+      c[j] = e4m3x2(tx, ty);
     }
+    o[0] = c[0] | (c[1] << 16);
+    o[1] = c[2] | (c[3] << 16);
+    sure = near >= 9u * 4096u && least >= 0.015625f && all == all;
   }
-};
+  return sure ? make_uint2(o[0], o[1]) : codes_near<FMT, BF16>(v, s, inv);
+}
 
-struct Growth { int64_t base; int bytes; };   // codes to map with a warp's table
+// Larger magnitudes of two pairs (their sign bits are 0), NaN if either is.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ bool finite_pair(uint32_t m) {
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  return (m & 0xFFFFu) < kInf && (m >> 16) < kInf;
+}
+// Pair of the largest |x| of eight values, without those that are not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t top_of(uint4 v, bool& bad) {
+  uint32_t m = max_pair<BF16>(max_pair<BF16>(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                              max_pair<BF16>(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  if (!finite_pair<BF16>(m)) {
+    bad = true;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    m = 0;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = w[j] & 0x7FFFu, hi = w[j] & 0x7FFF0000u;
+      m = max_pair<BF16>(m, (finite_pair<BF16>(lo) ? lo : 0u) | (finite_pair<BF16>(hi) ? hi : 0u));
+    }
+  }
+  return m;
+}
 
-template <int FMT, bool BF16, int D>
-__global__ void __launch_bounds__(32 * kApWarps) kv_append_kernel(const KvAppendArgs A) {
-  __shared__ uint8_t lut[kApWarps][256];
-  __shared__ Growth grow[kApWarps];
-  __shared__ int long_row, long_end;
-  __shared__ float tops[kApWarps];
-  constexpr int TPL = 32 / (D / 8);
+template <int FMT, bool BF16, int D, int IT>
+__global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppendArgs A) {
+  constexpr int LPT = D / 8;                   // lanes of a token
+  constexpr int TPL = 32 / LPT;                // tokens of a round
+  constexpr int RW = IT * TPL;                 // rows of a warp
+  constexpr int ROWS = kApWarps * RW;          // rows of the window
+  constexpr int ALL = kApHalo + ROWS + kApHalo;
   constexpr float kTop = FMT == QNT_KV_INT8 ? 127.0f : 448.0f;
+  static_assert(ROWS <= kApThreads && ROWS % 32 == 0, "a thread per row, whole mask words");
+  __shared__ int slot_s[ALL];
+  __shared__ uint32_t brk_s[ALL / 32];         // bit: the row does not go on from the row before
+  __shared__ uint32_t top_s[kApHalo + ROWS];   // max |x| of the run that begins at a row
+  __shared__ uint8_t refused_s[kApHalo + ROWS];
+  __shared__ short start_s[ROWS];              // where the row's run begins; -1: not written
+  __shared__ float scale_s[ROWS], inv_s[ROWS];
+  __shared__ int grow_row[ROWS], grow_n;
+  __shared__ float grow_old[ROWS];
+  __shared__ uint8_t lut_s[kApWarps][256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y, kv = blockIdx.z;
-  const int row = blockIdx.x * kApWarps + warp;
-  if (tid == 0) long_row = -1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __syncthreads();
-
-  const int P = A.page;
-  const long long limit = (long long)A.pages * P;
+  const int w0 = blockIdx.x * ROWS;            // first token row
+  const int P = A.page, pl = 31 - __clz(P);
   uint8_t* const codes = kv ? A.codes[1] : A.codes[0];
   float* const scales = kv ? A.scales[1] : A.scales[0];
-  const uint16_t* const x = static_cast<const uint16_t*>(kv ? A.x[1] : A.x[0]) + (int64_t)h * D;
-  auto slot_at = [&](int r) -> int { return r >= 0 && r < A.tokens ? A.slots[r] : -1; };
-  auto place = [&](int slot) -> int64_t {          // first byte of a slot's values
-    return (((int64_t)(slot / P) * A.heads + h) * P + slot % P) * D;
+  const uint16_t* const x = static_cast<const uint16_t*>(kv ? A.x[1] : A.x[0]) + (int64_t)h * D + 8 * (lane % LPT);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  uint4 v[IT];
+  const int mine = warp * RW + lane / LPT;     // this lane's first row in the window
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int row = w0 + mine + i * TPL;
+    v[i] = row < A.tokens ? ldg_cg128(x + (int64_t)row * A.stride) : make_uint4(0, 0, 0, 0);
+  }
+  const int limit = A.pages << pl;
+  for (int i = tid; i < ALL; i += kApThreads) {
+    const int row = w0 - kApHalo + i;
+    const int s = row >= 0 && row < A.tokens ? A.slots[row] : -1;
+    slot_s[i] = s < limit ? s : kApBad;
+    if (s >= limit && (h | kv) == 0) report(A.status, QNT_ERR_ARG);
+    if (i < kApHalo + ROWS) {
+      top_s[i] = 0;
+      refused_s[i] = 0;
+    }
+  }
+  if (tid == 0) grow_n = 0;
+  __syncthreads();
+
+  // ---- runs
+  for (int i = tid; i < ALL; i += kApThreads) {
+    const int s = slot_s[i], p = i ? slot_s[i - 1] : -1;
+    const bool on = s >= 0 && s != kApBad && p >= 0 && p + 1 == s && (s & (P - 1)) != 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, !on);
+    if (lane == 0) brk_s[i >> 5] = m;
+  }
+  __syncthreads();
+  const int idx = kApHalo + tid;               // this thread's row, for tid < ROWS
+  int start = -1;
+  float s0 = 0.0f;
+  if (tid < ROWS) {                            // whole warps
+    const int s = slot_s[idx];
+    const bool live = s >= 0 && s != kApBad;
+    if (live) {
+      int word = idx >> 5;
+      uint32_t m = brk_s[word] & (0xFFFFFFFFu >> (31 - (idx & 31)));
+      while (!m) m = brk_s[--word];            // a run is at most a page long
+      start = 32 * word + 31 - __clz(m);
+      if (slot_s[start] & (P - 1)) s0 = scales[(int64_t)(s >> pl) * A.heads + h];
+    }
+    // the run is refused if its page had one before it with only skipped rows in between
+    const int prev = start > 0 ? slot_s[start - 1] : -1;
+    const bool first = live && (idx == start || tid == 0);
+    bool refuse = first && prev >= 0 && (prev >> pl) == (s >> pl);
+    uint32_t look = __ballot_sync(0xffffffffu, first && prev < 0);
+    while (look) {
+      const int src = __ffs(look) - 1;
+      look &= look - 1;
+      const int page = __shfl_sync(0xffffffffu, s, src) >> pl;
+      int found = -1;
+      for (int at = w0 - kApHalo + __shfl_sync(0xffffffffu, start, src) - 2; found < 0 && at >= 0; at -= 256) {
+        int near = 256;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {         // rows at - 255 .. at, the nearest counts
+          const int r = at - 32 * i - lane;
+          if (r >= 0 && A.slots[r] >= 0) near = 32 * i + lane;
+        }
+        near = __reduce_min_sync(0xffffffffu, near);
+        if (near < 256) found = A.slots[at - near];
+      }
+      if (lane == src && found >= 0 && (found >> pl) == page) refuse = true;
+    }
+    if (refuse) {
+      refused_s[start] = 1;
+      if ((h | kv) == 0) report(A.status, QNT_ERR_ARG);
+    }
+    start_s[tid] = (short)start;
+  }
+  __syncthreads();
+  if (start >= 0 && refused_s[start]) start = start_s[tid] = -1;
+  __syncthreads();
+
+  // ---- max |x| of the runs: what a lane's rows of one run have in common is
+  // reduced over the token's lanes once
+  bool bad = false;
+  auto flush = [&](uint32_t m, int st) {
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) m = max_pair<BF16>(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = max(m & 0xFFFFu, m >> 16);
+    if (lane % LPT == 0 && st >= 0) atomicMax(top_s + st, BF16 ? m << 16 : __float_as_uint(h2f(m)));
   };
-  // the run's final scale; a larger one than the page had goes on record
-  auto settle = [&](int slot, float top, float& s0) -> float {
-    const float s_new = top / kTop;
-    float* const sp = scales + (int64_t)(slot / P) * A.heads + h;
-    s0 = slot % P ? *sp : 0.0f;
+  {
+    uint32_t m = 0;
+    int st = start_s[mine];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int now = i ? start_s[mine + i * TPL] : st;
+      if (__any_sync(0xffffffffu, now != st)) {
+        flush(m, st);
+        m = 0;
+        st = now;
+      }
+      bool odd = false;
+      m = max_pair<BF16>(m, top_of<BF16>(v[i], odd));
+      bad |= odd && now >= 0;
+    }
+    flush(m, st);
+  }
+  // rows of a run that crosses an end of the window
+  const int st_first = start_s[0], st_last = start_s[ROWS - 1];
+  const int back = st_first >= 0 ? max(kApHalo - st_first, 0) : 0;
+  int fwd = 0;
+  if (st_last >= 0) {
+    int word = (kApHalo + ROWS) >> 5;
+    while (word < ALL / 32 && !brk_s[word]) ++word;
+    fwd = word < ALL / 32 ? 32 * word + __ffs(brk_s[word]) - 1 - (kApHalo + ROWS) : kApHalo;
+  }
+#pragma unroll 4
+  for (int t = warp * TPL; t < back + fwd; t += kApWarps * TPL) {
+    const int k = t + lane / LPT;
+    const int row = k < back ? w0 - back + k : w0 + ROWS + (k - back);
+    bool odd = false;                          // reported by the row's own window
+    flush(top_of<BF16>(k < back + fwd ? ldg_cg128(x + (int64_t)row * A.stride) : make_uint4(0, 0, 0, 0), odd),
+          k < back + fwd ? (k < back ? st_first : st_last) : -1);
+  }
+  if (bad) report(A.status, QNT_ERR_NONFINITE);
+  __syncthreads();
+
+  // ---- scales
+  if (start >= 0) {
+    const float s = fmaxf(__uint_as_float(top_s[start]) / kTop, s0);
+    scale_s[tid] = s;
+    inv_s[tid] = s > 1e-30f && s < 1e30f ? 1.0f / s : s == 0.0f ? 0.0f : __int_as_float(0x7FC00000);
+    if (idx == start) {
+      const int slot = slot_s[idx];
+      scales[(int64_t)(slot >> pl) * A.heads + h] = s;
+      if ((slot & (P - 1)) && s > s0) {
+        const int k = atomicAdd(&grow_n, 1);
+        grow_row[k] = tid;
+        grow_old[k] = s0;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- codes
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int row = mine + i * TPL;
+    if (start_s[row] < 0) continue;
+    const int slot = slot_s[kApHalo + row];
+    const uint2 o = codes_of<FMT, BF16>(v[i], scale_s[row], inv_s[row]);
+    uint8_t* const dst = codes + (((((int64_t)(slot >> pl)) * A.heads + h) << pl) + (slot & (P - 1))) * D + 8 * (lane % LPT);
+    *reinterpret_cast<uint2*>(dst) = o;
+  }
+  // ---- the tokens before a run whose page's scale grew, 16 codes a lane and step
+  for (int k = warp; k < grow_n; k += kApWarps) {
+    const int row = grow_row[k], slot = slot_s[kApHalo + row];
     __syncwarp();
-    const float s = fmaxf(s_new, s0);
-    if (lane == 0) *sp = s;
-    return s;
-  };
-  auto tabulate = [&](int w, float s0, float s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t b = 8 * lane + i;
-      lut[w][b] = (uint8_t)requant_byte<FMT>(b, s0, s);
+      lut_s[warp][b] = (uint8_t)requant_byte<FMT>(b, grow_old[k], scale_s[row]);
     }
-  };
-
-  // does this warp's row begin a run, and where does the run end?
-  const int slot = slot_at(row);
-  int prev = slot_at(row - 1);
-  const bool next_to = prev >= 0;
-  bool head = slot >= 0 && slot < limit;
-  // a page's token rows with only skipped rows in between are found out, too
-  for (int at = row - 2; head && prev < 0 && at >= 0; at -= 256) {
-    int found = -1;
-#pragma unroll
-    for (int i = 7; i >= 0; --i) {                           // rows at - 255 .. at, the nearest counts
-      const int v = slot_at(at - 32 * i - lane);
-      if (v >= 0) found = 32 * i + lane;
-    }
-    const int nearest = __reduce_min_sync(0xffffffffu, found < 0 ? 256 : found);
-    if (nearest < 256) prev = slot_at(at - nearest);
-  }
-  if (slot >= limit && lane == 0 && h == 0) report(A.status, QNT_ERR_ARG);
-  if (head && prev >= 0 && prev / P == slot / P) {           // the row before is of the same page:
-    head = false;                                            // the run goes on from there,
-    if (!(next_to && prev + 1 == slot) && lane == 0 && h == 0) report(A.status, QNT_ERR_ARG);   // or this is a second one
-  }
-  int end = row;
-  if (head) {
-    const int most = P - slot % P;                           // to the end of the page
-    end = row + 1;
-    for (int k = 1; k < most; k += 32) {
-      const bool on = k + lane < most && slot_at(row + k + lane) == slot + k + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, on);
-      end += __ffs(~m) ? __ffs(~m) - 1 : 32;
-      if (~m) break;
-    }
-    if (end - row > kApShort && lane == 0) {
-      long_row = row;
-      long_end = end;
-    }
-  }
-  if (lane == 0) grow[warp].bytes = 0;
-  if (head && end - row <= kApShort) {
-    Share<BF16, D, (kApShort + TPL - 1) / TPL> sh;
-    sh.load(x, A.stride, row, end, TPL, lane);
-    sh.reduce();
-    if (sh.bad) report(A.status, QNT_ERR_NONFINITE);
-    float s0;
-    const float s = settle(slot, sh.top, s0);
-    sh.template store<FMT>(codes + place(slot), row, s, row, end, TPL, lane);
-    if (slot % P && s > s0) {
-      tabulate(warp, s0, s);
-      if (lane == 0) grow[warp] = {place(slot - slot % P), (slot % P) * D};
-    }
-  }
-  __syncthreads();
-  if (long_row >= 0) {
-    // the CTA's warps take TPL tokens each, in turn
-    constexpr int IT = 128 / (kApWarps * TPL);
-    const int r0 = long_row, e0 = long_end, first = A.slots[r0];
-    const int t = r0 + warp * TPL;
-    Share<BF16, D, IT> sh;
-    sh.load(x, A.stride, t, e0, kApWarps * TPL, lane);
-    sh.reduce();
-    if (sh.bad) report(A.status, QNT_ERR_NONFINITE);
-    if (lane == 0) tops[warp] = sh.top;
-    float* const sp = scales + (int64_t)(first / P) * A.heads + h;
-    const float s0 = first % P ? *sp : 0.0f;
-    __syncthreads();                                         // every warp has read the old scale
-    float top = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kApWarps; ++w) top = fmaxf(top, tops[w]);
-    const float s = fmaxf(top / kTop, s0);
-    if (tid == 0) *sp = s;
-    sh.template store<FMT>(codes + place(first), r0, s, t, e0, kApWarps * TPL, lane);
-    const int owner = long_row % kApWarps;
-    if (first % P && s > s0 && warp == owner) {
-      tabulate(owner, s0, s);
-      if (lane == 0) grow[owner] = {place(first - first % P), (first % P) * D};
-    }
-    __syncthreads();
-  }
-  // the tokens before a run whose page's scale grew, 16 codes a thread and step
-  for (int w = 0; w < kApWarps; ++w) {
-    const Growth g = grow[w];
-    for (int i = tid * 16; i < g.bytes; i += 32 * kApWarps * 16) {
-      uint4* const p = reinterpret_cast<uint4*>(codes + g.base + i);
-      const uint4 v = *p;
-      uint32_t in[4] = {v.x, v.y, v.z, v.w}, out[4];
+    __syncwarp();
+    uint8_t* const page = codes + (((((int64_t)(slot >> pl)) * A.heads + h) << pl)) * D;
+    const int bytes = (slot & (P - 1)) * D;
+#pragma unroll 4
+    for (int i = 16 * lane; i < bytes; i += 512) {
+      uint4* const p = reinterpret_cast<uint4*>(page + i);
+      const uint4 c = *p;
+      const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+      uint32_t out[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        out[j] = (uint32_t)lut[w][in[j] & 255u] | ((uint32_t)lut[w][(in[j] >> 8) & 255u] << 8) |
-                 ((uint32_t)lut[w][(in[j] >> 16) & 255u] << 16) | ((uint32_t)lut[w][in[j] >> 24] << 24);
+        out[j] = (uint32_t)lut_s[warp][in[j] & 255u] | ((uint32_t)lut_s[warp][(in[j] >> 8) & 255u] << 8) |
+                 ((uint32_t)lut_s[warp][(in[j] >> 16) & 255u] << 16) | ((uint32_t)lut_s[warp][in[j] >> 24] << 24);
       *p = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
 
-template <int FMT, bool BF16, int D>
+template <int FMT, bool BF16, int D, int IT>
 cudaError_t ap_launch(const KvAppendArgs& a, cudaStream_t s) {
+  constexpr int ROWS = kApWarps * IT * (256 / D);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.tokens + kApWarps - 1) / kApWarps, a.heads, 2);
-  cfg.blockDim = dim3(32 * kApWarps);
+  cfg.gridDim = dim3((a.tokens + ROWS - 1) / ROWS, a.heads, 2);
+  cfg.blockDim = dim3(kApThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_append_kernel<FMT, BF16, D>, a);
+  return cudaLaunchKernelEx(&cfg, kv_append_kernel<FMT, BF16, D, IT>, a);
+}
+
+template <int FMT, bool BF16, int D>
+cudaError_t ap_rounds(const KvAppendArgs& a, cudaStream_t s) {
+  // eight rounds a warp once that fills every SM; few rows are spread wider
+  const long long windows = ((long long)a.tokens + 8 * kApWarps * (256 / D) - 1) / (8 * kApWarps * (256 / D));
+  return windows * a.heads * 2 >= num_sms() ? ap_launch<FMT, BF16, D, 8>(a, s) : ap_launch<FMT, BF16, D, D == 256 ? 4 : 2>(a, s);
 }
 
 template <int FMT, bool BF16>
 cudaError_t ap_dim(int dim, const KvAppendArgs& a, cudaStream_t s) {
   switch (dim) {
-    case 64: return ap_launch<FMT, BF16, 64>(a, s);
-    case 128: return ap_launch<FMT, BF16, 128>(a, s);
-    default: return ap_launch<FMT, BF16, 256>(a, s);
+    case 64: return ap_rounds<FMT, BF16, 64>(a, s);
+    case 128: return ap_rounds<FMT, BF16, 128>(a, s);
+    default: return ap_rounds<FMT, BF16, 256>(a, s);
   }
 }
 
