@@ -85,7 +85,7 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const qnt_kv_desc& d, const KvAppendArgs& a, int xbf16, cudaStream_t s);
 
-// Attention over the key/value cache (kv_attn.cu).
+// Attention over the key/value cache (kv_attn.cu, kv_attn_tc.cu).
 struct KvAttnArgs {
   const uint8_t *kcodes, *vcodes;
   const float *kscales, *vscales;
@@ -99,8 +99,9 @@ struct KvAttnArgs {
   int heads, group;      // key/value heads, query heads of each
   int page_log2, pages, window;
   float scale_log2;      // scale * log2(e)
+  int narrow;            // most query rows of a key/value head that the narrow kernel takes
 };
 size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new);
-cudaError_t launch_kv_attn(const qnt_kv_desc& d, const KvAttnArgs& a, int max_new, int xbf16, cudaStream_t s);
+cudaError_t launch_kv_attn(const qnt_kv_desc& d, KvAttnArgs a, int max_new, int xbf16, cudaStream_t s);
 
 }  // namespace qnt

@@ -34,9 +34,8 @@
 //    warps take the tokens of its part in turn and are merged in shared memory; a
 //    (request, head) that spans several CTAs is merged by the one that arrives
 //    last (one counter), in CTA order, so the result does not depend on timing.
-#include <cuda_runtime.h>
-#include "common.cuh"
-#include "kernels.h"
+#include <climits>
+#include "kv_attn.cuh"
 
 namespace qnt {
 namespace {
@@ -44,9 +43,6 @@ namespace {
 constexpr int kKaWarps = 4;
 constexpr int kKaThreads = 32 * kKaWarps;
 constexpr int kKaMaxPerSm = 4;                    // CTAs per SM of any variant
-constexpr size_t kKaCounters = 16384;             // bytes in front of the partial results
-constexpr float kKaFloor = -1e30f;                // reference before the first token
-constexpr float kKaSlack = 8.0f;                  // log2 of the largest p
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -57,26 +53,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t pair16) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(pair16));
-  return d;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16_hi(uint32_t w) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(w));
   return d;
 }
 // Four consecutive codes of one token: (0, 1) and (2, 3).
@@ -124,7 +100,7 @@ __device__ __forceinline__ KaRow ka_row(const KvAttnArgs& A, int b) {
   w.begin = A.window ? max(w.len - w.n + 1 - A.window, 0) & ~31 : 0;
   w.tiles = (int)(((long long)w.n * A.group + ROWS - 1) / ROWS);
   w.units = max(1, (w.len - w.begin + UNIT - 1) / UNIT);
-  w.all = (long long)w.tiles * w.units * A.heads;
+  w.all = (long long)w.n * A.group > A.narrow ? 0 : (long long)w.tiles * w.units * A.heads;
   return w;
 }
 
@@ -238,10 +214,9 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[nr][c][i] << 16)), fabsf(__uint_as_float(q[nr][c][i] & 0xFFFF0000u))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = (int)((__float_as_uint(top) >> 23) & 255u);        // biased exponent
-        const int k = e == 0 || e == 255 ? 0 : min(max(14 - (e - 127), -126), 126);
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        factor *= __uint_as_float((uint32_t)(127 - k) << 23);
+        float up, down;
+        f16_range(top, up, down);
+        factor *= down;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -493,15 +468,9 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
       }
     __syncthreads();
     auto put = [&](int row, int d, float4 v, float sum) {    // the row's output, four values from d
-      const float f = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+      const float f = inv_sum(sum);
       const int t = (row0 + row) / A.group, hq = h * A.group + (row0 + row) % A.group;
-      uint2 out;
-      if (BF16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * f, v.y * f), z = __floats2bfloat162_rn(v.z * f, v.w * f);
-        out = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&z));
-      } else {
-        out = make_uint2(pack_f16(v.x * f, v.y * f), pack_f16(v.z * f, v.w * f));
-      }
+      const uint2 out = pack_out<BF16>(make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + (int64_t)(w.first + t) * A.y_stride + (int64_t)hq * D + d) = out;
     };
     const bool whole = u0 == 0 && u1 == w.units;
@@ -536,7 +505,7 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
     if (!whole) {
       // the CTAs first .. last share the job; the one that arrives last merges
       const long long u_first = pos - u0, u_last = u_first + w.units - 1;
-      const int first = (int)(((u_first + 1) * ctas - 1) / total), last = (int)(((u_last + 1) * ctas - 1) / total);
+      const int first = cta_of(u_first, ctas, total), last = cta_of(u_last, ctas, total);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -603,17 +572,31 @@ cudaError_t ka_dim(int dim, const KvAttnArgs& a, long long rows, cudaStream_t s)
   }
 }
 
+// Requests of up to so many query rows a key/value head go to this file's kernel
+// where some have more.
+constexpr int kKaNarrow = 64;
+
 }  // namespace
 
 size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new) {
-  (void)heads;
-  (void)max_new;
   const size_t rows = d.dim == 256 ? 8 : 16;
-  return kKaCounters + (size_t)num_sms() * kKaMaxPerSm * 2 * rows * (d.dim + 2) * 4;
+  size_t parts = (size_t)num_sms() * kKaMaxPerSm * 2 * rows * (d.dim + 2) * 4;
+  if ((long long)max_new * (heads / d.heads) > kKaNarrow) {
+    const size_t wide = (size_t)num_sms() * 2 * kv_attn_tc_part_bytes(d.dim);
+    if (wide > parts) parts = wide;
+  }
+  return kKaCounters + parts;
 }
 
-cudaError_t launch_kv_attn(const qnt_kv_desc& d, const KvAttnArgs& a, int max_new, int xbf16, cudaStream_t s) {
-  const long long rows = (long long)max_new * a.group;
+cudaError_t launch_kv_attn(const qnt_kv_desc& d, KvAttnArgs a, int max_new, int xbf16, cudaStream_t s) {
+  long long rows = (long long)max_new * a.group;
+  a.narrow = INT_MAX;
+  if (rows > kKaNarrow) {
+    a.narrow = kKaNarrow;
+    rows = 16;
+    const cudaError_t e = launch_kv_attn_tc(d, a, xbf16, s);
+    if (e != cudaSuccess) return e;
+  }
   if (d.fmt == QNT_KV_INT8)
     return xbf16 ? ka_dim<QNT_KV_INT8, true>(d.dim, a, rows, s) : ka_dim<QNT_KV_INT8, false>(d.dim, a, rows, s);
   return xbf16 ? ka_dim<QNT_KV_E4M3, true>(d.dim, a, rows, s) : ka_dim<QNT_KV_E4M3, false>(d.dim, a, rows, s);

@@ -401,14 +401,18 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  *              (qnt_kv_slots' d_len_out).
  *   d_table    device int32 [rows][width].
  *   max_new    the largest n as far as the caller knows it (>= 1): it chooses the
- *              kernel, not the result.
- *   d_work     device, qnt_kv_attn_work_bytes bytes, 16-byte aligned, zeroed by
- *              the caller before its first use; every call leaves it ready for
- *              the next.  Two calls that may run at the same time need two.
+ *              kernel, not what is computed.
+ *   d_work     device, qnt_kv_attn_work_bytes bytes for these heads and max_new,
+ *              16-byte aligned, zeroed by the caller before its first use; every
+ *              call leaves it ready for the next, of whatever sizes it is large
+ *              enough for.  Two calls that may run at the same time need two.
  * Products are of exact fp16 operands with fp32 accumulation (q is rescaled by a
  * power of two per row where it is bf16), the softmax is fp32, its weights are
  * rounded to fp16 for the second product, relative to a running maximum, and y
- * once to its type.  The bytes of tokens that no query sees may be anything; a
+ * once to its type.  (Requests of more than 64 query rows a key/value head, on the
+ * tcgen05 tensor cores: a weight also carries its page's V scale; in pages whose
+ * V scale is less than 2^-8 of another's in the same 128 tokens its absolute
+ * error is 2^-25 of the larger.)  The bytes of tokens that no query sees may be anything; a
  * visible E4M3 byte must not be 0x7F or 0xFF (NaN; qnt_kv_append writes none).
  * A page number outside the cache is read as page 0, and d_len beyond
  * width * page is cut there (QNT_ERR_ARG in *d_status).

@@ -501,3 +501,13 @@ def test_decode_steps_together(fmt, xdt):
         err = np.abs(y.double().cpu().numpy().reshape(T, heads, dim) - ref)
         assert (err[live] <= bound[live]).all(), float((err / bound)[live].max())
     assert int(st) == 0
+
+
+# ------------------------------------------------------------------ many query rows (tensor-memory kernel)
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+@pytest.mark.parametrize("xdt", [0, 1])
+@pytest.mark.parametrize("dim,page,kv_heads,group,lens,news,window", [
+    (128, 64, 1, 4, [5], [5], 0), (128, 16, 1, 4, [40], [33], 0), (64, 32, 2, 8, [300, 17], [40, 17], 0), (256, 128, 1, 4, [200, 64, 1], [64, 40, 1], 0),
+    (128, 16, 2, 7, [129, 30, 260], [5, 3, 41], 0), (64, 16, 1, 16, [90, 400], [16, 33], 50), (256, 16, 1, 1, [700], [150], 100), (128, 32, 1, 3, [700, 9], [300, 0], 130)])
+def test_attn_many_query_rows(fmt, xdt, dim, page, kv_heads, group, lens, news, window):
+    check_attn(make_attn(3 * dim + page + group, fmt, xdt, page, kv_heads, group, dim, lens, news, window=window))
