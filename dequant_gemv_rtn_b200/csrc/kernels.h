@@ -99,6 +99,7 @@ struct KvAttnArgs {
   int heads, group;      // key/value heads, query heads of each
   int page_log2, pages, window;
   float scale_log2;      // scale * log2(e)
+  uint32_t group_mul, group_shift;   // row / group = (row * group_mul >> 32) >> group_shift, for 2 <= group, row < 2^31
   int narrow;            // most query rows of a key/value head that the narrow kernel takes
 };
 size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new);

@@ -40,8 +40,7 @@
 namespace qnt {
 namespace {
 
-constexpr int kKaWarps = 4;
-constexpr int kKaThreads = 32 * kKaWarps;
+constexpr int kKaBatch = 10;                      // parts of a split job that a thread reads at once
 constexpr int kKaMaxPerSm = 4;                    // CTAs per SM of any variant
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -104,8 +103,9 @@ __device__ __forceinline__ KaRow ka_row(const KvAttnArgs& A, int b) {
   return w;
 }
 
-template <int FMT, bool BF16, int D, int NR, int PER_SM>
-__global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAttnArgs A) {
+template <int FMT, bool BF16, int D, int NR, int W, int PER_SM>
+__global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArgs A) {
+  constexpr int kKaWarps = W, kKaThreads = 32 * W;
   constexpr int ROWS = 8 * NR;                              // query rows of a CTA
   constexpr int TT = (D == 256 || NR > 1) ? 16 : 32;        // tokens of a warp's step
   constexpr int NB = TT / 16;
@@ -115,11 +115,14 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
   constexpr int MT = D / 16;                                // m-tiles of O^T
   constexpr int LD = D + 4;
   extern __shared__ __align__(16) float sm[];
-  float* const o_s = sm;                                    // [kKaWarps][ROWS][LD]
-  float* const m_s = sm + kKaWarps * ROWS * LD;             // [kKaWarps][ROWS]
+  float* const o_s = sm + 64;                               // [kKaWarps][ROWS][LD]
+  float* const m_s = o_s + kKaWarps * ROWS * LD;            // [kKaWarps][ROWS]
   float* const l_s = m_s + kKaWarps * ROWS;
-  __shared__ long long part[kKaWarps], start_off;
-  __shared__ int start_row, last_s;
+  long long* const part = reinterpret_cast<long long*>(sm); // a sum per warp, in the first 64 words
+  long long& start_off = part[16];
+  int& start_row = reinterpret_cast<int*>(sm)[34];
+  int& last_s = reinterpret_cast<int*>(sm)[35];
+  static_assert(W <= 16, "scan scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, r = lane & 3;
   const int pl = A.page_log2, P = 1 << pl;
@@ -151,7 +154,8 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
   if (total == 0) return;
   const long long ctas = min((long long)gridDim.x, total);
   if (blockIdx.x >= ctas) return;
-  const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+  const KaParts parts(total, ctas);
+  const long long lo = parts.begin(blockIdx.x), hi = parts.begin(blockIdx.x + 1);
   if (lo >= end - mine && lo < end) {
     long long at = end - mine;
     int b = b0;
@@ -176,83 +180,15 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
       off -= w.all;
       w = ka_row<ROWS, UNIT>(A, ++b);
     }
-    const int job = (int)(off / w.units), u0 = (int)(off % w.units);
+    const int job = (int)div_units(off, w.units), u0 = (int)(off - (long long)job * w.units);
     const int u1 = (int)min((long long)w.units, u0 + (hi - pos));
-    const int h = job / w.tiles, row0 = (job % w.tiles) * ROWS;
+    const int h = job / w.tiles, row0 = (job - h * w.tiles) * ROWS;
     const int rows = min(ROWS, w.n * A.group - row0);       // query rows of this job
     const int base = w.len - w.n;                           // position of the first new token
-    const int t_first = row0 / A.group, t_last = (row0 + rows - 1) / A.group;
+    const int t_first = token_of(A, row0), t_last = token_of(A, row0 + rows - 1);
     const int lo_tok = w.begin + u0 * UNIT;
     const int hi_tok = min(min(w.begin + u1 * UNIT, w.len), base + t_last + 1);   // behind the last that a row sees
     const int32_t* const table = A.table + (size_t)b * A.width;
-
-    // ---- the query rows as the MMAs' B operand, in fp16
-    uint32_t q[NR][C][8];
-    float c0[NR][2], init[NR][2];                           // rows 2r, 2r + 1: factor of the logits, -128 sum of q
-    int sees[NR][2];                                        // last visible token
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      const int row = 8 * nr + g;
-      const bool live = row < rows;
-      const int t = (row0 + row) / A.group, hq = h * A.group + (row0 + row) % A.group;
-      const uint16_t* const src = static_cast<const uint16_t*>(A.q) + (int64_t)(w.first + t) * A.q_stride + (int64_t)hq * D + 16 * r;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const uint4 x = live ? ldg_cg128(src + 64 * c) : make_uint4(0, 0, 0, 0);
-        const uint4 z = live ? ldg_cg128(src + 64 * c + 8) : make_uint4(0, 0, 0, 0);
-        q[nr][c][0] = x.x; q[nr][c][1] = x.y; q[nr][c][2] = x.z; q[nr][c][3] = x.w;
-        q[nr][c][4] = z.x; q[nr][c][5] = z.y; q[nr][c][6] = z.z; q[nr][c][7] = z.w;
-      }
-      float factor = A.scale_log2;
-      if (BF16) {
-        // a power of two brings the row's largest |q| into [2^14, 2^15)
-        float top = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[nr][c][i] << 16)), fabsf(__uint_as_float(q[nr][c][i] & 0xFFFF0000u))));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        float up, down;
-        f16_range(top, up, down);
-        factor *= down;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            q[nr][c][i] = pack_f16(__uint_as_float(q[nr][c][i] << 16) * up, __uint_as_float(q[nr][c][i] & 0xFFFF0000u) * up);
-      }
-      float sum = 0.0f;
-      if (FMT == QNT_KV_INT8) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum += h2f(q[nr][c][i] & 0xFFFFu) + h2f(q[nr][c][i] >> 16);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        factor *= 16777216.0f;                              // codes are q 2^-24
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {                          // row n's values are in the lanes with g = n
-        c0[nr][i] = __shfl_sync(0xffffffffu, factor, (2 * r + i) * 4);
-        init[nr][i] = FMT == QNT_KV_INT8 ? -128.0f / 16777216.0f * __shfl_sync(0xffffffffu, sum, (2 * r + i) * 4) : 0.0f;
-        sees[nr][i] = base + (row0 + 8 * nr + 2 * r + i) / A.group;
-      }
-    }
-
-    float o[NR][MT][4], l[NR][4], m[NR][2], corr[NR][2];
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[nr][i][k] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) l[nr][k] = 0.0f;
-      m[nr][0] = m[nr][1] = kKaFloor;
-      corr[nr][0] = corr[nr][1] = 0.0f;
-    }
 
     // ---- tokens, TT at a time
     int page[NB];
@@ -315,13 +251,83 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
       }
     };
 
-    int tk = lo_tok + warp * TT;
-    if (tk < hi_tok) {
-      load_pages(tk);
-      load_k(tk);
-      load_v(tk);
-      load_pages(tk + UNIT);
+    // ---- the query rows as the MMAs' B operand, in fp16
+    uint32_t q[NR][C][8];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int row = 8 * nr + g;
+      const bool live = row < rows;
+      const int t = token_of(A, row0 + row), hq = h * A.group + row0 + row - t * A.group;
+      const uint16_t* const src = static_cast<const uint16_t*>(A.q) + (int64_t)(w.first + t) * A.q_stride + (int64_t)hq * D + 16 * r;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 x = live ? ldg_cg128(src + 64 * c) : make_uint4(0, 0, 0, 0);
+        const uint4 z = live ? ldg_cg128(src + 64 * c + 8) : make_uint4(0, 0, 0, 0);
+        q[nr][c][0] = x.x; q[nr][c][1] = x.y; q[nr][c][2] = x.z; q[nr][c][3] = x.w;
+        q[nr][c][4] = z.x; q[nr][c][5] = z.y; q[nr][c][6] = z.z; q[nr][c][7] = z.w;
+      }
     }
+    // the first step's codes are requested before the queries have to be there
+    int tk = lo_tok + warp * TT;
+    load_pages(tk);
+    load_k(tk);
+    load_v(tk);
+    load_pages(tk + UNIT);
+    float c0[NR][2], init[NR][2];                           // rows 2r, 2r + 1: factor of the logits, -128 sum of q
+    int sees[NR][2];                                        // last visible token
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      float factor = A.scale_log2;
+      if (BF16) {
+        // a power of two brings the row's largest |q| into [2^14, 2^15)
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[nr][c][i] << 16)), fabsf(__uint_as_float(q[nr][c][i] & 0xFFFF0000u))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float up, down;
+        f16_range(top, up, down);
+        factor *= down;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            q[nr][c][i] = pack_f16(__uint_as_float(q[nr][c][i] << 16) * up, __uint_as_float(q[nr][c][i] & 0xFFFF0000u) * up);
+      }
+      float sum = 0.0f;
+      if (FMT == QNT_KV_INT8) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum += h2f(q[nr][c][i] & 0xFFFFu) + h2f(q[nr][c][i] >> 16);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        factor *= 16777216.0f;                              // codes are q 2^-24
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {                          // row n's values are in the lanes with g = n
+        c0[nr][i] = __shfl_sync(0xffffffffu, factor, (2 * r + i) * 4);
+        init[nr][i] = FMT == QNT_KV_INT8 ? -128.0f / 16777216.0f * __shfl_sync(0xffffffffu, sum, (2 * r + i) * 4) : 0.0f;
+        sees[nr][i] = base + token_of(A, row0 + 8 * nr + 2 * r + i);
+      }
+    }
+
+    float o[NR][MT][4], l[NR][4], m[NR][2], corr[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[nr][i][k] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) l[nr][k] = 0.0f;
+      m[nr][0] = m[nr][1] = kKaFloor;
+      corr[nr][0] = corr[nr][1] = 0.0f;
+    }
+
     for (; tk < hi_tok; tk += UNIT) {
       // S^T = K Q^T
       float s[NB][NR][4];
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
     __syncthreads();
     auto put = [&](int row, int d, float4 v, float sum) {    // the row's output, four values from d
       const float f = inv_sum(sum);
-      const int t = (row0 + row) / A.group, hq = h * A.group + (row0 + row) % A.group;
+      const int t = token_of(A, row0 + row), hq = h * A.group + row0 + row - t * A.group;
       const uint2 out = pack_out<BF16>(make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + (int64_t)(w.first + t) * A.y_stride + (int64_t)hq * D + d) = out;
     };
@@ -505,34 +511,45 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
     if (!whole) {
       // the CTAs first .. last share the job; the one that arrives last merges
       const long long u_first = pos - u0, u_last = u_first + w.units - 1;
-      const int first = cta_of(u_first, ctas, total), last = cta_of(u_last, ctas, total);
-      __threadfence();
+      const int first = parts.cta_of(u_first), last = parts.cta_of(u_last);
       __syncthreads();
       if (tid == 0) {
-        const uint32_t before = atomicAdd(counters + first, 1u);
+        // releases what the CTA wrote, acquires what the others did
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counters + first) : "memory");
         last_s = before == (uint32_t)(last - first);
         if (last_s) counters[first] = 0;                     // ready for the next call
-        __threadfence();
       }
       __syncthreads();
       if (last_s) {
+        auto at = [&](int c) { return partials + (size_t)(2 * c + (c == first ? 1 : 0)) * PART; };
         for (int i = tid; i < rows * (D / 4); i += kKaThreads) {
           const int row = i / (D / 4), d = 4 * (i % (D / 4));
-          auto at = [&](int c) { return partials + (size_t)(2 * c + (c == first ? 1 : 0)) * PART; };
-          float top = kKaFloor;
-#pragma unroll 8
-          for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(at(c) + ROWS * D + row));
-          float sum = 0.0f;
+          float top = kKaFloor, sum = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-          for (int c = first; c <= last; ++c) {
-            const float f = exp2_approx(__ldcg(at(c) + ROWS * D + row) - top);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(at(c) + row * D + d));
-            sum = fmaf(f, __ldcg(at(c) + ROWS * D + ROWS + row), sum);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
+          for (int c = first; c <= last; c += kKaBatch) {     // a batch of parts is requested at once
+            float pm[kKaBatch], pl_[kKaBatch];
+            float4 po[kKaBatch];
+#pragma unroll
+            for (int k = 0; k < kKaBatch; ++k) {
+              const float* const src = at(min(c + k, last));
+              pm[k] = __ldcg(src + ROWS * D + row);
+              pl_[k] = __ldcg(src + ROWS * D + ROWS + row);
+              po[k] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
+            }
+            float most = top;
+#pragma unroll
+            for (int k = 0; k < kKaBatch; ++k) most = fmaxf(most, pm[k]);
+            const float by = exp2_approx(top - most);
+            top = most;
+            sum *= by;
+            v = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+#pragma unroll
+            for (int k = 0; k < kKaBatch; ++k) {
+              const float f = c + k <= last ? exp2_approx(pm[k] - top) : 0.0f;
+              sum = fmaf(f, pl_[k], sum);
+              v = make_float4(fmaf(f, po[k].x, v.x), fmaf(f, po[k].y, v.y), fmaf(f, po[k].z, v.z), fmaf(f, po[k].w, v.w));
+            }
           }
           put(row, d, v, sum);
         }
@@ -544,15 +561,15 @@ __global__ void __launch_bounds__(kKaThreads, PER_SM) kv_attn_kernel(const KvAtt
   }
 }
 
-template <int FMT, bool BF16, int D, int NR>
-cudaError_t ka_launch(const KvAttnArgs& a, cudaStream_t s) {
-  constexpr int PER_SM = D == 64 && NR == 1 ? 4 : D == 256 ? 2 : 3;
-  static_assert(PER_SM <= kKaMaxPerSm, "workspace");
-  auto kfn = kv_attn_kernel<FMT, BF16, D, NR, PER_SM>;
+template <int FMT, bool BF16, int D, int NR, int W, int PER_SM>
+cudaError_t ka_launch_w(const KvAttnArgs& a, cudaStream_t s) {
+  auto kfn = kv_attn_kernel<FMT, BF16, D, NR, W, PER_SM>;
+  cudaError_t e = configure_smem(reinterpret_cast<const void*>(kfn));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms() * PER_SM);
-  cfg.blockDim = dim3(kKaThreads);
-  cfg.dynamicSmemBytes = (size_t)kKaWarps * 8 * NR * (D + 4 + 2) * 4;
+  cfg.blockDim = dim3(32 * W);
+  cfg.dynamicSmemBytes = 256 + (size_t)W * 8 * NR * (D + 4 + 2) * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -561,14 +578,26 @@ cudaError_t ka_launch(const KvAttnArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kfn, a);
 }
+template <int FMT, bool BF16, int D, int NR>
+cudaError_t ka_launch(const KvAttnArgs& a, long long rows, cudaStream_t s) {
+  constexpr int PER_SM = D == 64 && NR == 1 ? 4 : D == 256 ? 2 : 3;
+  static_assert(PER_SM <= kKaMaxPerSm, "workspace");
+  // A few long jobs are cut into many parts each; one large CTA per SM then leaves a
+  // third of the parts to merge (one row of 131072 tokens on 8 heads: 60 -> 53 us),
+  // while with many jobs small CTAs overlap one's start and end with another's
+  // tokens (64 rows on 8 heads: 193 us, large CTAs 224; 32 jobs: 8.9, 9.4).
+  const long long tiles = (rows + 8 * NR - 1) / (8 * NR);
+  if ((long long)a.rows * a.heads * tiles < 32) return ka_launch_w<FMT, BF16, D, NR, 4 * PER_SM, 1>(a, s);
+  return ka_launch_w<FMT, BF16, D, NR, 4, PER_SM>(a, s);
+}
 
 template <int FMT, bool BF16>
 cudaError_t ka_dim(int dim, const KvAttnArgs& a, long long rows, cudaStream_t s) {
   // up to 16 query rows share a pass where their accumulators fit in registers
   switch (dim) {
-    case 64: return rows <= 8 ? ka_launch<FMT, BF16, 64, 1>(a, s) : ka_launch<FMT, BF16, 64, 2>(a, s);
-    case 128: return rows <= 8 ? ka_launch<FMT, BF16, 128, 1>(a, s) : ka_launch<FMT, BF16, 128, 2>(a, s);
-    default: return ka_launch<FMT, BF16, 256, 1>(a, s);
+    case 64: return rows <= 8 ? ka_launch<FMT, BF16, 64, 1>(a, rows, s) : ka_launch<FMT, BF16, 64, 2>(a, rows, s);
+    case 128: return rows <= 8 ? ka_launch<FMT, BF16, 128, 1>(a, rows, s) : ka_launch<FMT, BF16, 128, 2>(a, rows, s);
+    default: return ka_launch<FMT, BF16, 256, 1>(a, rows, s);
   }
 }
 
@@ -591,9 +620,12 @@ size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new) {
 cudaError_t launch_kv_attn(const qnt_kv_desc& d, KvAttnArgs a, int max_new, int xbf16, cudaStream_t s) {
   long long rows = (long long)max_new * a.group;
   a.narrow = INT_MAX;
+  // row / group by a product: mul = ceil(2^(32 + shift) / group), 2^shift < group <= 2^(shift + 1)
+  for (a.group_shift = 0; (2 << a.group_shift) < a.group; ++a.group_shift) {}
+  a.group_mul = a.group > 1 ? (uint32_t)((((uint64_t)1 << (32 + a.group_shift)) + a.group - 1) / a.group) : 0;
   if (rows > kKaNarrow) {
     a.narrow = kKaNarrow;
-    rows = 16;
+    rows = kKaNarrow;
     const cudaError_t e = launch_kv_attn_tc(d, a, xbf16, s);
     if (e != cudaSuccess) return e;
   }

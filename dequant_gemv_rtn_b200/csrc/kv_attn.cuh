@@ -49,9 +49,26 @@ __device__ __forceinline__ uint2 pack_out(float4 v) {
 // 1 / sum of the weights; 0 for a row that sees nothing.
 __device__ __forceinline__ float inv_sum(float sum) { return sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum; }
 
-// CTA whose part [c total / ctas, (c + 1) total / ctas) of the units holds unit u.
-__device__ __forceinline__ int cta_of(long long u, long long ctas, long long total) {
-  return (int)(((u + 1) * ctas - 1) / total);
+// n / d: 64-bit divisions take ten times as long and are rarely needed.
+__device__ __forceinline__ long long div_units(long long n, long long d) {
+  return ((n | d) >> 32) == 0 ? (long long)((uint32_t)n / (uint32_t)d) : n / d;
+}
+// `total` units cut into parts for `ctas` CTAs, the first ones a unit longer.
+struct KaParts {
+  long long each, longer;       // units of a part; CTAs with one more
+  __device__ __forceinline__ KaParts(long long total, long long ctas) {
+    each = ctas ? div_units(total, ctas) : 0;
+    longer = total - each * ctas;
+  }
+  __device__ __forceinline__ long long begin(long long c) const { return c * each + min(c, longer); }
+  __device__ __forceinline__ int cta_of(long long u) const {   // whose part holds unit u
+    const long long split = longer * (each + 1);
+    return (int)(u < split ? div_units(u, each + 1) : longer + div_units(u - split, each));
+  }
+};
+// Query row -> token and back: row / group, group = A.group.
+__device__ __forceinline__ int token_of(const KvAttnArgs& A, int row) {
+  return A.group == 1 ? row : (int)(__umulhi((uint32_t)row, A.group_mul) >> A.group_shift);
 }
 
 // The wide kernel (kv_attn_tc.cu): requests of more than `narrow` query rows a head.

@@ -79,8 +79,8 @@ struct KtTile { int t_first, t_last, begin, end, units; };
 // Tokens that the rows [row0, row0 + cap) of a request see.
 __device__ __forceinline__ KtTile kt_tile(const KvAttnArgs& A, const KtRow& w, int row0, int cap) {
   KtTile t;
-  t.t_first = row0 / A.group;
-  t.t_last = (min(w.rows, row0 + cap) - 1) / A.group;
+  t.t_first = token_of(A, row0);
+  t.t_last = token_of(A, min(w.rows, row0 + cap) - 1);
   const int base = w.len - w.n;
   t.begin = A.window ? max(base + t.t_first + 1 - A.window, 0) & ~15 : 0;
   t.end = min(w.len, base + t.t_last + 1);
@@ -120,8 +120,8 @@ struct KtWalk {
       off -= w.all;
       w = kt_row<CAP>(A, ++b);
     }
-    j.h = (int)(off / w.per_head);
-    int u = (int)(off % w.per_head), k = 0;
+    j.h = (int)div_units(off, w.per_head);
+    int u = (int)(off - j.h * w.per_head), k = 0;
     for (;; ++k) {
       j.t = kt_tile(A, w, k * CAP, CAP);
       if (u < j.t.units) break;
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
   }
   const long long ctas = min((long long)gridDim.x, total);
   const bool busy = blockIdx.x < ctas;
-  const long long lo = busy ? blockIdx.x * total / ctas : 0, hi = busy ? (blockIdx.x + 1) * total / ctas : 0;
+  const KaParts parts(total, ctas);
+  const long long lo = busy ? parts.begin(blockIdx.x) : 0, hi = busy ? parts.begin(blockIdx.x + 1) : 0;
   if (busy && lo >= end - mine && lo < end) {
     long long at = end - mine;
     int b = b0;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       const bool live = kKtRows * s + r < job.rows;
       const bool on = kKtRows * s < job.rows;                 // the stream has rows
       alone = job.rows <= kKtRows;
-      const int t = row / A.group, hq = job.h * A.group + row % A.group;
+      const int t = token_of(A, row), hq = job.h * A.group + row - t * A.group;
       float m = kKaFloor, l = 0.0f, unit = 0.0f;
       bool has_unit = false, ok = true;
       if (on) {
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
         __syncwarp();
         const int sees = live ? job.base + t : -1;
         // a tile has something to hide if it ends behind all_see or begins at or before hidden
-        const int all_see = job.base + (job.row0 + kKtRows * s) / A.group;
-        const int hidden = A.window ? job.base + (job.row0 + min(job.rows, kKtRows * (s + 1)) - 1) / A.group - A.window : INT_MIN;
+        const int all_see = job.base + token_of(A, job.row0 + kKtRows * s);
+        const int hidden = A.window ? job.base + token_of(A, job.row0 + min(job.rows, kKtRows * (s + 1)) - 1) - A.window : INT_MIN;
         int tok0 = job.t.begin + job.u0 * kKtTok;
 
         // two streams compute their weights in turn: while one does, the other's products
@@ -599,8 +600,8 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       float* const partials = reinterpret_cast<float*>(static_cast<uint8_t*>(A.work) + kKaCounters);
       uint16_t* const y = static_cast<uint16_t*>(A.y);
       auto out_at = [&](int rr) {                             // place of the job's row rr in y
-        const int q = job.row0 + rr, tt = q / A.group;
-        return y + (int64_t)(slot.walk.w.first + tt) * A.y_stride + (int64_t)(job.h * A.group + q % A.group) * D;
+        const int q = job.row0 + rr, tt = token_of(A, q);
+        return y + (int64_t)(slot.walk.w.first + tt) * A.y_stride + (int64_t)(job.h * A.group + q - tt * A.group) * D;
       };
       if (on && ok) {
         const float f = whole ? exp2_approx(unit) * inv_sum(l) : exp2_approx(unit);
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       if (!whole) {
         // the CTAs first .. last share the job; the one that arrives last merges
         uint32_t* const counters = static_cast<uint32_t*>(A.work);
-        const int first = cta_of(job.u_first, ctas, total), last = cta_of(job.u_first + job.t.units - 1, ctas, total);
+        const int first = parts.cta_of(job.u_first), last = parts.cta_of(job.u_first + job.t.units - 1);
         __threadfence();
         asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
         if (tid == 0) {
