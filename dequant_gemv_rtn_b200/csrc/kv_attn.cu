@@ -352,6 +352,10 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
           }
         }
       }
+      float ks_now[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) ks_now[nb] = ks[nb];
+      load_k(tk + UNIT);                                     // with the pages read a step ahead
       // base-2 logits, relative to the reference
       float over = 0.0f;
       const bool edge = tk + TT - 1 > base + t_first || (A.window && tk <= base + t_last - A.window);
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[nb][nr][k] *= c0[nr][k & 1] * ks[nb];
+          for (int k = 0; k < 4; ++k) s[nb][nr][k] *= c0[nr][k & 1] * ks_now[nb];
       if (edge) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -412,7 +416,6 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
           p[nb][nr][0] = transpose8x8(pack_f16(e[0], e[1]));
           p[nb][nr][1] = transpose8x8(pack_f16(e[2], e[3]));
         }
-      load_k(tk + UNIT);                                     // with the pages read a step ahead
       if (FMT == QNT_KV_E4M3 && tk + TT > w.len) {           // bytes behind the last token may be NaN
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
