@@ -160,11 +160,6 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t block
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((block >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 // Packed fp32 pairs (one rounding each).
 __device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
   uint64_t d;
@@ -481,9 +476,14 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
               unit = lv;
             }
           }
-          // the weights, 32 columns at a time; P's columns 16 q .. 16 q + 15 lie in S's that are read already
-          turn_wait();
-          float sum = 0.0f, alpha = 1.0f;
+          auto hide = [&](uint32_t (&v)[32], int q) {          // what the row does not see becomes -infinity
+            const int hi_k = sees - tok0 - 32 * q, lo_k = A.window ? hi_k - A.window : INT_MIN;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k > hi_k || k <= lo_k) v[k] = 0xFF800000u;
+          };
+          // the tile's maximum, 32 columns at a time, before the stream's turn
+          float top = m;
 #pragma unroll 1
           for (int q2 = 0; q2 < kKtTok / 32; q2 += 2) {
 #pragma unroll
@@ -492,16 +492,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
               uint32_t(&v)[32] = x[b];
               tmem_wait_ld32(v);
               if (q + 1 < kKtTok / 32) tmem_ld32(ts + 32u * (uint32_t)(q + 1), x[b ^ 1]);
-              if (edge) {                                     // what the row does not see becomes -infinity
-                const int hi_k = sees - tok0 - 32 * q, lo_k = A.window ? hi_k - A.window : INT_MIN;
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (k > hi_k || k <= lo_k) v[k] = 0xFF800000u;
-              }
-              const float2 f0 = *reinterpret_cast<const float2*>(sc + 2 * q), f1 = *reinterpret_cast<const float2*>(sc + 2 * q + 1);
-              const float ca = factor(c0, f0.x), cb = factor(c0, f1.x);
-              // (a V scale of 0: the weights count, the values do not)
-              const bool none0 = f0.y == -INFINITY, none1 = f1.y == -INFINITY;
+              if (edge) hide(v, q);
               float most[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -509,55 +500,53 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
 #pragma unroll
                 for (int j = 1; j < 8; ++j) most[k] = fmaxf(most[k], __uint_as_float(v[8 * k + j]));
               }
-              const float top = fmaxf(fmaxf(most[0], most[1]) * ca, fmaxf(most[2], most[3]) * cb);
-              float e[32];
-              for (;;) {
-#pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                  const float c = h2 ? cb : ca;
-                  const float ref = (h2 ? none1 : none0) ? m : m - ((h2 ? f1.y : f0.y) - unit);
-                  const uint64_t c2 = pair_f32(c, c), ref2 = pair_f32(-ref, -ref);
-#pragma unroll
-                  for (int k = 16 * h2; k < 16 * h2 + 16; k += 2) {
-                    unpair_f32(fma_f32x2(pair_u32(v[k], v[k + 1]), c2, ref2), e[k], e[k + 1]);
-                    e[k] = exp2_approx(e[k]);
-                    e[k + 1] = exp2_approx(e[k + 1]);
-                  }
-                }
-                if (!__any_sync(0xffffffffu, top > m + kKaSlack)) break;
-                // the reference moves: with it what is summed and written of this tile
-                const float to_top = fmaxf(m, top), by = exp2_approx(m - to_top);
-                m = to_top;
-                alpha *= by;
-                sum *= by;
-                const uint32_t by2 = pack_f16(by, by);
-                tmem_wait_st();
+              top = fmaxf(top, fmaxf(fmaxf(most[0], most[1]) * factor(c0, sc[2 * q].x), fmaxf(most[2], most[3]) * factor(c0, sc[2 * q + 1].x)));
+            }
+          }
+          tmem_ld32(ts, x[0]);
+          float alpha = 1.0f;
+          if (__any_sync(0xffffffffu, top > m + kKaSlack)) {
+            alpha = exp2_approx(m - top);
+            m = top;
+          }
+          // the weights; P's columns 16 q .. 16 q + 15 lie in S's that are read already
+          turn_wait();
+          float sum = 0.0f;
 #pragma unroll 1
-                for (int k = 0; k < 16 * q; k += 16) {
-                  uint32_t p[32];
-                  tmem_ld32(ts + (uint32_t)k, p);             // (16 columns of P, and 16 more)
-                  tmem_wait_ld32(p);
+          for (int q2 = 0; q2 < kKtTok / 32; q2 += 2) {
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) p[j] = hmul2(p[j], by2);
-                  tmem_st16(ts + (uint32_t)k, *reinterpret_cast<uint32_t(*)[16]>(p));
-                }
-              }
+            for (int b = 0; b < 2; ++b) {
+              const int q = q2 + b;
+              uint32_t(&v)[32] = x[b];
+              tmem_wait_ld32(v);
+              if (q + 1 < kKtTok / 32) tmem_ld32(ts + 32u * (uint32_t)(q + 1), x[b ^ 1]);
+              if (edge) hide(v, q);
               uint32_t p[16];
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
-                const float* const w = e + 16 * h2;
-                const bool none = h2 ? none1 : none0;
-                uint64_t part0 = pair_f32(w[0], w[1]), part1 = pair_f32(w[2], w[3]);
+                const float2 f = *reinterpret_cast<const float2*>(sc + 2 * q + h2);
+                const float c = factor(c0, f.x);
+                const bool none = f.y == -INFINITY;           // V's scale is 0: the weights count, the values do not
+                const float ref = none ? m : m - (f.y - unit);
+                const uint64_t c2 = pair_f32(c, c), ref2 = pair_f32(-ref, -ref);
+                float e[16];
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  unpair_f32(fma_f32x2(pair_u32(v[16 * h2 + k], v[16 * h2 + k + 1]), c2, ref2), e[k], e[k + 1]);
+                  e[k] = exp2_approx(e[k]);
+                  e[k + 1] = exp2_approx(e[k + 1]);
+                }
+                uint64_t part0 = pair_f32(e[0], e[1]), part1 = pair_f32(e[2], e[3]);
 #pragma unroll
                 for (int k = 4; k < 16; k += 4) {
-                  part0 = add_f32x2(part0, pair_f32(w[k], w[k + 1]));
-                  part1 = add_f32x2(part1, pair_f32(w[k + 2], w[k + 3]));
+                  part0 = add_f32x2(part0, pair_f32(e[k], e[k + 1]));
+                  part1 = add_f32x2(part1, pair_f32(e[k + 2], e[k + 3]));
                 }
                 float s0, s1;
                 unpair_f32(add_f32x2(part0, part1), s0, s1);
-                sum = fmaf(s0 + s1, none ? 1.0f : exp2_approx(unit - (h2 ? f1.y : f0.y)), sum);
+                sum = fmaf(s0 + s1, none ? 1.0f : exp2_approx(unit - f.y), sum);
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) p[8 * h2 + k / 2] = none ? 0u : pack_f16(w[k], w[k + 1]);
+                for (int k = 0; k < 16; k += 2) p[8 * h2 + k / 2] = none ? 0u : pack_f16(e[k], e[k + 1]);
               }
               tmem_st16(ts + 16u * (uint32_t)q, p);
             }
