@@ -638,22 +638,57 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
         asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
         if (*last_s) {
           auto at = [&](int c) { return partials + (size_t)(2 * c + (c == first ? 1 : 0)) * PART; };
-          for (int x = tid; x < job.rows * (D / 4); x += 32 * T::SoftWarps) {
-            const int rr = x / (D / 4), d = 4 * (x % (D / 4));
-            float top = kKaFloor;
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(at(c) + CAP * D + rr));
-            float sum = 0.0f;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) {
-              const float f = exp2_approx(__ldcg(at(c) + CAP * D + rr) - top);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(at(c) + rr * D + d));
-              sum = fmaf(f, __ldcg(at(c) + CAP * D + CAP + rr), sum);
-              v = make_float4(fmaf(f, o.x, v.x), fmaf(f, o.y, v.y), fmaf(f, o.z, v.z), fmaf(f, o.w, v.w));
+          constexpr int TH = 32 * T::SoftWarps;                 // a thread per row
+          constexpr int FIT = T::Tile * NS / (4 * CAP);         // parts whose factors fit in Q's place
+          float* const f_s = reinterpret_cast<float*>(smem + kKtCtrl);   // [part][row]
+          const int n = last - first + 1;
+          float top = kKaFloor, sum = 0.0f;                     // of row tid
+          if (tid < job.rows) {
+#pragma unroll 8
+            for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(at(first + c) + CAP * D + tid));
+#pragma unroll 8
+            for (int c = 0; c < n; ++c) {
+              const float f = exp2_approx(__ldcg(at(first + c) + CAP * D + tid) - top);
+              sum = fmaf(f, __ldcg(at(first + c) + CAP * D + CAP + tid), sum);
             }
-            const float f = inv_sum(sum);
-            *reinterpret_cast<uint2*>(out_at(rr) + d) = pack_out<BF16>(make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+          }
+          const float inv = inv_sum(sum);
+          constexpr int U = 8;                                  // pieces of four values that a thread has in flight
+          for (int c0 = 0; c0 < n; c0 += FIT) {                 // (one round, unless over a hundred parts)
+            const int cn = min(FIT, n - c0);
+            asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+            if (tid < job.rows)
+#pragma unroll 8
+              for (int c = 0; c < cn; ++c)
+                f_s[c * CAP + tid] = exp2_approx(__ldcg(at(first + c0 + c) + CAP * D + tid) - top) * inv;
+            asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+            for (int x0 = tid; x0 < job.rows * (D / 4); x0 += U * TH) {
+              float4 v[U];
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int x = x0 + u * TH;
+                if (c0 && x < job.rows * (D / 4)) v[u] = *reinterpret_cast<const float4*>(at(first) + 4 * x);
+              }
+#pragma unroll 2
+              for (int c = 0; c < cn; ++c) {
+                const float* const src = at(first + c0 + c);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  const int x = min(x0 + u * TH, job.rows * (D / 4) - 1);
+                  const float f = f_s[c * CAP + x / (D / 4)];
+                  const float4 o = __ldcg(reinterpret_cast<const float4*>(src + 4 * x));
+                  v[u] = make_float4(fmaf(f, o.x, v[u].x), fmaf(f, o.y, v[u].y), fmaf(f, o.z, v[u].z), fmaf(f, o.w, v[u].w));
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int x = x0 + u * TH, rr = x / (D / 4), d = 4 * (x % (D / 4));
+                if (x >= job.rows * (D / 4)) break;
+                if (c0 + cn < n) *reinterpret_cast<float4*>(at(first) + 4 * x) = v[u];   // goes on in the next round
+                else *reinterpret_cast<uint2*>(out_at(rr) + d) = pack_out<BF16>(v[u]);
+              }
+            }
           }
           asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");   // last_s is read
         }

@@ -511,3 +511,14 @@ def test_decode_steps_together(fmt, xdt):
     (128, 16, 2, 7, [129, 30, 260], [5, 3, 41], 0), (64, 16, 1, 16, [90, 400], [16, 33], 50), (256, 16, 1, 1, [700], [150], 100), (128, 32, 1, 3, [700, 9], [300, 0], 130)])
 def test_attn_many_query_rows(fmt, xdt, dim, page, kv_heads, group, lens, news, window):
     check_attn(make_attn(3 * dim + page + group, fmt, xdt, page, kv_heads, group, dim, lens, news, window=window))
+
+
+@pytest.mark.parametrize("fmt,xdt,dim,group,len_,new", [(R.E4M3, 0, 64, 8, 20011, 9), (R.INT8, 1, 128, 4, 9001, 130), (R.INT8, 0, 256, 4, 7003, 33), (R.E4M3, 1, 128, 65, 20011, 1)])
+def test_attn_many_query_rows_split(fmt, xdt, dim, group, len_, new):
+    """One request on one key/value head is shared by every CTA; twice with one workspace, bit for bit alike."""
+    Q = H.q()
+    c = make_attn(len_ + dim, fmt, xdt, 64, 1, group, dim, [len_, 70], [new, 1])
+    work = H.dev_bytes(Q.qnt_kv_attn_work_bytes(Q.kv_desc(fmt, 64, c["pages"], 1, dim), c["heads"], new))
+    y = check_attn(c, work=work)
+    assert torch.equal(y, call_attn(c, work=work))
+    assert int(work[:16384].max()) == 0                    # ready for the next call
