@@ -19,9 +19,9 @@
 //    the A operand of O += P V; O stays in tensor memory.  A thread of the stream's
 //    first softmax warp issues its MMAs, which has nothing else to do by then.
 //  * Four warps per stream do the softmax, a thread a row, 32 columns at a time in
-//    a loop, packed fp32 arithmetic taking two logits at once.  Only if one passes
-//    the reference by 8 (2^8: fp16 takes it) is the reference moved, what is done of
-//    the tile rescaled, and O before its next product.
+//    two loops (the maximum; the weights), packed fp32 arithmetic taking two logits
+//    at once.  Only if one passes the reference by 8 (2^8: fp16 takes it) is the
+//    reference moved and O rescaled before its next product.
 //  * Scales: K's multiplies the row's factor, per 16 tokens (a page or a part of
 //    one).  V's goes into the exponent: the weight that meets V's codes is
 //    2^(x - m + log2(vs) - u), and a page's share of the sum is taken back by
@@ -34,13 +34,15 @@
 //    kv_attn.cu, here with each row tile's own causal range.
 //
 // Measured on two chunks of 1024 tokens, the cache 5000 and 8000 long (32 / 8 heads,
-// dim 128, INT8): 359 us, 560 TFLOP/s (the mma.sync kernel: 1268 us).  A tile takes
-// 5900 cycles, of which a stream's softmax 2900 and its two products 1500, one
-// after the other; two streams overlap them in part.  Slower were, in us: the loop
-// over a tile's columns unrolled, with the row in registers (437 to 570:
-// instruction fetch), two threads a row (400, lockstep; 595, spills), decoding in
-// the softmax warps (743: the streams wait for each other), a warp of its own for
-// the MMAs (404).
+// dim 128, INT8): 297 us, 676 TFLOP/s (the mma.sync kernel: 1268 us).  A tile takes
+// 5100 cycles, of which a stream's maximum 800, its weights 2200 (the other stream's
+// turn meanwhile is over or not begun) and its two products 1500.  Slower were, in
+// us: the loops over a tile's columns unrolled, with the row in registers (437 to
+// 570: instruction fetch), one pass with the weights corrected where the maximum
+// moved (359), no turns (371 against 343 then), two threads a row (400 and, with
+// the registers that leaves, 595), decoding in the softmax warps (743: the streams
+// wait for each other), a warp of its own for the MMAs (404).  A split job costs its
+// last CTA about 2 us a part (160 rows); two chunks of 40 tokens take 64 us.
 //
 // Every wait is bounded (2 s); on expiry the kernel reports QNT_ERR_TIMEOUT, every
 // role runs through without waiting, and tensor memory is freed after the last MMA.
@@ -405,12 +407,14 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
         // Q in fp16, bf16 rows scaled by a power of two; a negative factor goes into Q
         const uint16_t* const src = static_cast<const uint16_t*>(A.q) + (int64_t)(slot.walk.w.first + t) * A.q_stride + (int64_t)hq * D;
         float up = 1.0f, down = 1.0f;
-        if (BF16 && live) {
+        uint4 v[D / 8];                                       // the whole row at once: one wait for memory
+#pragma unroll
+        for (int p = 0; p < D / 8; ++p) v[p] = live ? ldg_cg128(src + 8 * p) : make_uint4(0, 0, 0, 0);
+        if (BF16) {
           float top = 0.0f;
-#pragma unroll 4
+#pragma unroll
           for (int p = 0; p < D / 8; ++p) {
-            const uint4 v = ldg_cg128(src + 8 * p);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
@@ -418,10 +422,9 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           f16_range(top, up, down);
         }
         const uint32_t flip = A.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll 4
+#pragma unroll
         for (int p = 0; p < D / 8; ++p) {
-          uint4 v = live ? ldg_cg128(src + 8 * p) : make_uint4(0, 0, 0, 0);
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (BF16) w[i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
@@ -643,24 +646,39 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           float* const f_s = reinterpret_cast<float*>(smem + kKtCtrl);   // [part][row]
           const int n = last - first + 1;
           float top = kKaFloor, sum = 0.0f;                     // of row tid
-          if (tid < job.rows) {
-#pragma unroll 8
-            for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(at(first + c) + CAP * D + tid));
-#pragma unroll 8
-            for (int c = 0; c < n; ++c) {
-              const float f = exp2_approx(__ldcg(at(first + c) + CAP * D + tid) - top);
-              sum = fmaf(f, __ldcg(at(first + c) + CAP * D + CAP + tid), sum);
+          auto batch = [&](int c0, int most, bool keep) {       // 16 parts' references and sums, in flight together
+            float pm[16], ps[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float* const src = at(first + min(c0 + k, most - 1)) + CAP * D + tid;
+              pm[k] = __ldcg(src);
+              ps[k] = __ldcg(src + CAP);
             }
-          }
+            float next = top;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) next = fmaxf(next, pm[k]);
+            sum *= exp2_approx(top - next);
+            top = next;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (c0 + k < most) {
+                sum = fmaf(exp2_approx(pm[k] - top), ps[k], sum);
+                if (keep) f_s[(c0 + k) * CAP + tid] = pm[k];
+              }
+          };
+          const bool mine_row = tid < job.rows;
+          if (mine_row)
+            for (int c = 0; c < n; c += 16) batch(c, n, c + 16 <= FIT);
           const float inv = inv_sum(sum);
           constexpr int U = 8;                                  // pieces of four values that a thread has in flight
-          for (int c0 = 0; c0 < n; c0 += FIT) {                 // (one round, unless over a hundred parts)
+          for (int c0 = 0; c0 < n; c0 += FIT) {                 // (one round, unless there are more parts)
             const int cn = min(FIT, n - c0);
-            asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
-            if (tid < job.rows)
-#pragma unroll 8
-              for (int c = 0; c < cn; ++c)
-                f_s[c * CAP + tid] = exp2_approx(__ldcg(at(first + c0 + c) + CAP * D + tid) - top) * inv;
+            if (c0) asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+            if (mine_row)
+              for (int c = 0; c < cn; ++c) {
+                const float pm = c0 ? __ldcg(at(first + c0 + c) + CAP * D + tid) : f_s[c * CAP + tid];
+                f_s[c * CAP + tid] = exp2_approx(pm - top) * inv;
+              }
             asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
             for (int x0 = tid; x0 < job.rows * (D / 4); x0 += U * TH) {
               float4 v[U];
