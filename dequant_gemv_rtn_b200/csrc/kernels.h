@@ -52,6 +52,8 @@ cudaError_t launch_gemv_seq_noalloc(const qnt_seq_step* steps, int n, int xbf16,
 void set_test_fault(int fault, unsigned long long timeout_ns);
 // Test builds only (gemm_tc.cu): the same for this thread's next tcgen05 GEMM launches.
 void set_test_gemm_fault(int fault, unsigned long long timeout_ns);
+// Test builds only (kv_attn_tc.cu): the same for this thread's next tcgen05 attention launches.
+void set_test_attn_fault(int fault, unsigned long long timeout_ns);
 #endif
 
 // An empty kernel: the next kernel in the stream cannot overlap the ones before it.
@@ -101,6 +103,8 @@ struct KvAttnArgs {
   float scale_log2;      // scale * log2(e)
   uint32_t group_mul, group_shift;   // row / group = (row * group_mul >> 32) >> group_shift, for 2 <= group, row < 2^31
   int narrow;            // most query rows of a key/value head that the narrow kernel takes
+  unsigned long long timeout_ns;   // limit of every wait (kv_attn_tc.cu)
+  int fault;             // test builds only: an injected fault (0: none)
 };
 size_t kv_attn_work_bytes(const qnt_kv_desc& d, int heads, int max_new);
 cudaError_t launch_kv_attn(const qnt_kv_desc& d, KvAttnArgs a, int max_new, int xbf16, cudaStream_t s);

@@ -73,6 +73,6 @@ __device__ __forceinline__ int token_of(const KvAttnArgs& A, int row) {
 
 // The wide kernel (kv_attn_tc.cu): requests of more than `narrow` query rows a head.
 size_t kv_attn_tc_part_bytes(int dim);            // a partial result
-cudaError_t launch_kv_attn_tc(const qnt_kv_desc& d, const KvAttnArgs& a, int xbf16, cudaStream_t s);
+cudaError_t launch_kv_attn_tc(const qnt_kv_desc& d, KvAttnArgs a, int xbf16, cudaStream_t s);
 
 }  // namespace qnt

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
   const int pl = A.page_log2, P = 1 << pl;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (gt_wait(bar, parity & 1u, abort_s, kKtTimeoutNs, 0)) return true;
+    if (gt_wait(bar, parity & 1u, abort_s, A.timeout_ns, 0)) return true;
     if (!*abort_s) {
       *abort_s = 1;
       report(A.status, QNT_ERR_TIMEOUT);
@@ -792,7 +792,13 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           store(k_s + stage * T::Tile, kreg);
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(k_full + stage);
+#ifdef QNT_TEST_FAULTS
+          // fault 1 (test builds): in CTA 0 a decode warp never reports the first tile of K
+          const bool skip = A.fault == 1 && blockIdx.x == 0 && it == 0 && dw == 1;
+#else
+          constexpr bool skip = false;
+#endif
+          if (lane == 0 && !skip) mbar_arrive(k_full + stage);
           if (i + 1 < ntiles) {
             load_pages(table, h, tok0 + kKtTok, end_tok);
             load(A.kcodes, h, tok0 + kKtTok, kreg);
@@ -819,6 +825,16 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tbase), "r"(kKtCols) : "memory");
   }
 }
+
+#ifdef QNT_TEST_FAULTS
+static thread_local int t_kt_fault = 0;
+static thread_local unsigned long long t_kt_timeout_ns = kKtTimeoutNs;
+#define QNT_KT_FAULT t_kt_fault
+#define QNT_KT_TIMEOUT t_kt_timeout_ns
+#else
+#define QNT_KT_FAULT 0
+#define QNT_KT_TIMEOUT kKtTimeoutNs
+#endif
 
 template <int FMT, bool BF16, int D>
 cudaError_t kt_launch(const KvAttnArgs& a, cudaStream_t s) {
@@ -854,7 +870,16 @@ cudaError_t kt_dim(int dim, const KvAttnArgs& a, cudaStream_t s) {
 
 size_t kv_attn_tc_part_bytes(int dim) { return (size_t)kKtRows * (dim == 256 ? 1 : 2) * (dim + 2) * 4; }
 
-cudaError_t launch_kv_attn_tc(const qnt_kv_desc& d, const KvAttnArgs& a, int xbf16, cudaStream_t s) {
+#ifdef QNT_TEST_FAULTS
+void set_test_attn_fault(int fault, unsigned long long timeout_ns) {
+  t_kt_fault = fault;
+  t_kt_timeout_ns = timeout_ns;
+}
+#endif
+
+cudaError_t launch_kv_attn_tc(const qnt_kv_desc& d, KvAttnArgs a, int xbf16, cudaStream_t s) {
+  a.timeout_ns = QNT_KT_TIMEOUT;
+  a.fault = QNT_KT_FAULT;
   if (d.fmt == QNT_KV_INT8) return xbf16 ? kt_dim<QNT_KV_INT8, true>(d.dim, a, s) : kt_dim<QNT_KV_INT8, false>(d.dim, a, s);
   return xbf16 ? kt_dim<QNT_KV_E4M3, true>(d.dim, a, s) : kt_dim<QNT_KV_E4M3, false>(d.dim, a, s);
 }

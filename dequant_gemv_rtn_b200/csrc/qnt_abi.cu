@@ -388,4 +388,22 @@ extern "C" int qnt_test_gemm_fault(const qnt_desc* desc, const void* d_codes, co
   qnt::set_test_gemm_fault(0, 2000000000ull);
   return rc;
 }
+
+// Test builds only: qnt_kv_attn (more than 64 query rows a key/value head: the
+// tcgen05 kernel) with a fault injected and a short wait limit.  fault 1: in CTA 0
+// one decode warp never reports the first tile of K; the waits behind it give up
+// after timeout_ns, every role runs through, and the kernel reports
+// QNT_ERR_TIMEOUT and frees its tensor memory.
+extern "C" int qnt_test_kv_attn_fault(const qnt_kv_desc* desc, const void* d_kcodes, const void* d_vcodes,
+                                      const float* d_kscales, const float* d_vscales, const void* d_q, int64_t q_stride,
+                                      void* d_y, int64_t y_stride, int heads, const int32_t* d_cu, const int32_t* d_len,
+                                      const int32_t* d_table, int rows, int width, int tokens, int max_new, float scale,
+                                      int window, void* d_work, int xdtype, int* d_status, void* stream, int fault,
+                                      unsigned long long timeout_ns) {
+  qnt::set_test_attn_fault(fault, timeout_ns);
+  const int rc = qnt_kv_attn(desc, d_kcodes, d_vcodes, d_kscales, d_vscales, d_q, q_stride, d_y, y_stride, heads, d_cu,
+                             d_len, d_table, rows, width, tokens, max_new, scale, window, d_work, xdtype, d_status, stream);
+  qnt::set_test_attn_fault(0, 2000000000ull);
+  return rc;
+}
 #endif

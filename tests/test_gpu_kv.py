@@ -522,3 +522,64 @@ def test_attn_many_query_rows_split(fmt, xdt, dim, group, len_, new):
     y = check_attn(c, work=work)
     assert torch.equal(y, call_attn(c, work=work))
     assert int(work[:16384].max()) == 0                    # ready for the next call
+
+
+def test_attn_wait_expires_and_next_call_is_correct():
+    """The tcgen05 kernel of the test build: in CTA 0 a decode warp never reports the first tile, so the waits behind it
+    expire (50 ms).  The call returns QNT_ERR_TIMEOUT in the status, has freed its tensor memory and leaves the
+    workspace ready: the next calls with it, the product library's and the test build's, are correct."""
+    import ctypes
+    import time
+    Q = H.q()
+    from dequant_gemv_rtn_b200 import build
+    f = ctypes.CDLL(build.build(test=True)).qnt_test_kv_attn_fault
+    P, I, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    f.restype, f.argtypes = I, [P, P, P, P, P, P, L, P, L, I, P, P, P, I, I, I, I, ctypes.c_float, I, P, I, P, P, I, ctypes.c_ulonglong]
+    c = make_attn(95, R.INT8, 0, 16, 2, 4, 128, [300, 5000], [40, 33])
+    d = Q.kv_desc(c["fmt"], c["page"], c["pages"], c["kv_heads"], c["dim"])
+    work = H.dev_bytes(Q.qnt_kv_attn_work_bytes(d, c["heads"], c["max_new"]))
+    row = c["heads"] * c["dim"]
+    q, gc, gs = c["q"].reshape(c["tokens"], row).cuda(), dev(c["codes"], torch.uint8), dev(c["scales"], torch.float32)
+    y, cu, ln, tb, st = torch.full_like(q, 3.0), dev(c["cu"]), dev(c["lens"]), dev(c["table"]), dev([0])
+
+    def call(fault, timeout_ns):
+        return f(ctypes.addressof(d), gc[0].data_ptr(), gc[1].data_ptr(), gs[0].data_ptr(), gs[1].data_ptr(), q.data_ptr(), row, y.data_ptr(), row, c["heads"],
+                 cu.data_ptr(), ln.data_ptr(), tb.data_ptr(), 2, c["width"], c["tokens"], c["max_new"], c["scale"], 0, work.data_ptr(), 0, st.data_ptr(),
+                 torch.cuda.current_stream().cuda_stream, fault, timeout_ns)
+
+    torch.cuda.synchronize()
+    t0 = time.time()
+    assert call(1, 50_000_000) == Q.QNT_OK
+    torch.cuda.synchronize()
+    assert int(st) == Q.QNT_ERR_TIMEOUT and 0.05 <= time.time() - t0 < 10.0
+    check_attn(c, work=work)
+    st.zero_()
+    y.fill_(3)
+    assert call(0, 2_000_000_000) == Q.QNT_OK
+    torch.cuda.synchronize()
+    c["status"] = int(st)
+    check_attn(c, y=y.reshape(c["tokens"], c["heads"], c["dim"]))
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+@pytest.mark.parametrize("new", [2, 50])
+def test_attn_scale_of_any_sign(scale, new):
+    c = make_attn(96, R.INT8, 1, 32, 1, 4, 64, [90, 200], [1, new])
+    c["scale"] = scale
+    check_attn(c)
+
+
+@pytest.mark.parametrize("dim,page,tokens", [(64, 32, 1300), (128, 16, 700), (256, 128, 330)])
+@pytest.mark.parametrize("fmt,xdt", [(R.INT8, 1), (R.E4M3, 0)])
+def test_append_prompts(dim, page, tokens, fmt, xdt):
+    """Enough rows for the wide windows: prompts of several pages, decode rows between them."""
+    r = np.random.default_rng(dim)
+    heads, runs, left = 16, [], tokens
+    while left > 0:
+        n = min(left, int(r.choice([1, 1, 3, page, 2 * page + 5, 7 * page + 1])))
+        runs.append((int(r.integers(0, page)), n))
+        left -= n
+    pages = sum(-(-(b % page + n) // page) for b, n in runs) + 2
+    slot = random_slots_of(r, page, pages, runs) + [-1] * 5
+    codes, scales = make_cache(4, fmt, pages, heads, page, dim)
+    check_append(fmt, xdt, page, dim, heads, codes, scales, values(9, len(slot), heads * dim, xdt), np.array(slot))
