@@ -661,7 +661,10 @@ def run_kernel_only(name: str, fmt_name: str, M: int = 16, repeats: int = 5):
         bf16 activation rows, `repeats` qnt_gemm launches;
       "quantize": qnt_quantize of the Llama-7B gate matrix (11008 x 4096 fp32);
       "int8_down": the INT8 per-channel down_proj (K=11008, N=4096), qnt_gemv;
-      "fp16_lm_head": the FP16 lm_head (K=4096, N=32000), qnt_gemv."""
+      "fp16_lm_head": the FP16 lm_head (K=4096, N=32000), qnt_gemv;
+      "kv_append": 8192 token rows into the key/value cache (8 heads of 128, INT8, pages of 64);
+      "kv_attn": one new token of each of 32 requests with 8192 cached (64 query, 8 key/value heads of 128, INT8);
+      "kv_attn_chunk": two chunks of 512 new tokens, 4096 cached (32 query, 8 key/value heads of 128, INT8)."""
     import torch
     from dequant_gemv_rtn_b200 import qnt as Q
     from dequant_gemv_rtn_b200 import synth
@@ -676,7 +679,31 @@ def run_kernel_only(name: str, fmt_name: str, M: int = 16, repeats: int = 5):
         return d, codes, meta
 
     shapes = []
-    if name == "gemm":
+    if name.startswith("kv_"):
+        rows, new, cached, heads = {"kv_append": (8, 1024, 1024, 32), "kv_attn": (32, 1, 8192, 64), "kv_attn_chunk": (2, 512, 4096, 32)}[name]
+        kv, dim, page, T = 8, 128, 64, rows * new
+        width = cached // page
+        d = Q.kv_desc(Q.QNT_KV_INT8, page, rows * width, kv, dim)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        table = torch.randperm(rows * width, device="cuda").to(torch.int32).view(rows, width)
+        cu = torch.arange(rows + 1, **i32) * new
+        length = torch.full((rows,), cached, **i32)
+        pos = cached - new + torch.arange(new, device="cuda")
+        slots = (table[:, pos // page] * page + pos % page).to(torch.int32).reshape(-1)
+        codes = torch.randint(1, 256, (2, Q.qnt_kv_codes_bytes(d)), dtype=torch.uint8, device="cuda")
+        scales = torch.rand((2, rows * width * kv), device="cuda") * 0.02 + 0.01
+        qkv = torch.randn(T, (heads + 2 * kv) * dim, device="cuda", dtype=torch.float16)
+        y = torch.empty(T, heads * dim, dtype=torch.float16, device="cuda")
+        work = torch.zeros(Q.qnt_kv_attn_work_bytes(d, heads, new), dtype=torch.uint8, device="cuda")
+        for _ in range(repeats):
+            if name == "kv_append":
+                Q.qnt_kv_append(d, codes[0], codes[1], scales[0], scales[1], qkv[:, heads * dim:], qkv[:, (heads + kv) * dim:], qkv.stride(0),
+                                slots, T, Q.QNT_F16, st)
+            else:
+                Q.qnt_kv_attn(d, codes[0], codes[1], scales[0], scales[1], qkv, qkv.stride(0), y, heads * dim, heads, cu, length, table, rows,
+                              width, T, new, dim ** -0.5, 0, work, Q.QNT_F16, st)
+        shapes, outs = [[rows, new, cached, heads, kv, dim]], [scales if name == "kv_append" else y]
+    elif name == "gemm":
         d, codes, meta = quantized(Q.QNT_INT4_ASYM, 28672, 8192, GROUP, 3)
         X = synth.activations_device(M, 8192, seed=5, dtype=torch.bfloat16)
         Y = torch.empty((M, 28672), dtype=torch.bfloat16, device="cuda")
@@ -729,7 +756,8 @@ def run_kernel_only(name: str, fmt_name: str, M: int = 16, repeats: int = 5):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel-only", default=None,
-                    choices=[n for n, _, _ in SHAPES] + ["layer", "gemm", "quantize", "int8_down", "fp16_lm_head"],
+                    choices=[n for n, _, _ in SHAPES] + ["layer", "gemm", "quantize", "int8_down", "fp16_lm_head", "kv_append", "kv_attn",
+                                                            "kv_attn_chunk"],
                     help="profiling case: a few launches of one kernel (see run_kernel_only)")
     ap.add_argument("--fmt", default="int4", help="format for --kernel-only with a layer shape")
     ap.add_argument("--m", type=int, default=16, help="activation rows for --kernel-only gemm")
