@@ -1,5 +1,5 @@
-// kv_attn.cuh -- what the two attention kernels share (kv_attn.cu: up to 16 query
-// rows of a key/value head; kv_attn_tc.cu: more).
+// kv_attn.cuh -- what the two attention kernels share (kv_attn.cu: few query rows
+// of a key/value head; kv_attn_tc.cu: many).
 #pragma once
 #include "common.cuh"
 #include "kernels.h"

@@ -1,7 +1,7 @@
 // kv_attn_tc.cu -- attention of many query rows over the paged 8-bit key/value
 // cache on the 5th-generation tensor cores (qnt_kv_attn; definition in
 // include/qnt.h): requests whose new tokens x query heads of a key/value head are
-// more than 64 rows, that is prompt chunks and long drafts on shared heads.
+// many rows, that is prompt chunks and long drafts on shared heads.
 //
 // With 128 rows every cached byte meets 256 flops and more, so the tensor cores,
 // the exponentials (128 x 128 of them a tile at 16 a cycle take as long as the

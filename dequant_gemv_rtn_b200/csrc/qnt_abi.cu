@@ -389,8 +389,8 @@ extern "C" int qnt_test_gemm_fault(const qnt_desc* desc, const void* d_codes, co
   return rc;
 }
 
-// Test builds only: qnt_kv_attn (more than 64 query rows a key/value head: the
-// tcgen05 kernel) with a fault injected and a short wait limit.  fault 1: in CTA 0
+// Test builds only: qnt_kv_attn (many query rows a key/value head: the tcgen05
+// kernel) with a fault injected and a short wait limit.  fault 1: in CTA 0
 // one decode warp never reports the first tile of K; the waits behind it give up
 // after timeout_ns, every role runs through, and the kernel reports
 // QNT_ERR_TIMEOUT and frees its tensor memory.

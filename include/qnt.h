@@ -302,6 +302,7 @@ int qnt_gemv_seq_noalloc(const qnt_seq_step* steps, int nsteps, int xdtype, int*
  * code value * scale.  INT8 byte = q + 128 with q in -127..127 (zero-extended
  * bytes are fp16 subnormals, the operand of the tensor cores); E4M3 byte =
  * the OCP 8-bit float (sign, 4 exponent, 3 mantissa bits, largest value 448).
+ * Scales are finite and not negative.
  * A token's slot is page * (tokens in a page) + its place in the page.
  */
 typedef enum { QNT_KV_INT8 = 1, QNT_KV_E4M3 = 2 } qnt_kv_fmt;
@@ -409,11 +410,12 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  * Products are of exact fp16 operands with fp32 accumulation (q is rescaled by a
  * power of two per row where it is bf16), the softmax is fp32, its weights are
  * rounded to fp16 for the second product, relative to a running maximum, and y
- * once to its type.  (Requests of more than 64 query rows a key/value head, on the
- * tcgen05 tensor cores: a weight also carries its page's V scale; in pages whose
- * V scale is less than 2^-8 of another's in the same 128 tokens its absolute
- * error is 2^-25 of the larger.)  The bytes of tokens that no query sees may be anything; a
- * visible E4M3 byte must not be 0x7F or 0xFF (NaN; qnt_kv_append writes none).
+ * once to its type.  (Requests of more than 32 query rows a key/value head may go to
+ * the tcgen05 tensor cores.  There a weight also carries its page's V scale: in
+ * pages whose V scale is less than 2^-8 of another's in the same 128 tokens its
+ * absolute error is 2^-25 of the larger.)  The bytes of tokens that no query sees
+ * may be anything; a visible E4M3 byte must not be 0x7F or 0xFF (NaN;
+ * qnt_kv_append writes none).
  * A page number outside the cache is read as page 0, and d_len beyond
  * width * page is cut there (QNT_ERR_ARG in *d_status).
  */
