@@ -102,7 +102,7 @@ __device__ __forceinline__ KaRow ka_row(const KvAttnArgs& A, int b) {
   w.first = min(max(A.cu[b], 0), A.tokens);
   w.n = min(max(A.cu[b + 1], w.first), A.tokens) - w.first;
   w.len = min(max(A.len[b], 0), A.width << A.page_log2);
-  w.begin = A.window ? max(w.len - w.n + 1 - A.window, 0) & ~31 : 0;
+  w.begin = A.window ? max(w.len - w.n + 1 - A.window, 0) & ~15 : 0;   // no page before the window is looked up
   w.tiles = (int)(((long long)w.n * A.group + ROWS - 1) / ROWS);
   w.units = max(1, (w.len - w.begin + UNIT - 1) / UNIT);
   w.all = (long long)w.n * A.group > A.narrow ? 0 : (long long)w.tiles * w.units * A.heads;

@@ -583,3 +583,16 @@ def test_append_prompts(dim, page, tokens, fmt, xdt):
     slot = random_slots_of(r, page, pages, runs) + [-1] * 5
     codes, scales = make_cache(4, fmt, pages, heads, page, dim)
     check_append(fmt, xdt, page, dim, heads, codes, scales, values(9, len(slot), heads * dim, xdt), np.array(slot))
+
+
+def test_attn_window_needs_no_page_before_it():
+    """Pages that lie wholly before every new token's window may be gone (their table entries -1)."""
+    for new, group in ((1, 4), (3, 4), (60, 4)):
+        c = make_attn(97, R.INT8, 0, 16, 1, group, 128, [700, 350], [new, 1], window=100)
+        for b in range(2):
+            first = max(0, int(c["lens"][b]) - int(c["cu"][b + 1] - c["cu"][b]) + 1 - 100) // 16
+            c["table"][b, :first] = -1
+        y = call_attn(c)
+        assert c["status"] == 0
+        full = dict(c, table=np.where(c["table"] < 0, 0, c["table"]))
+        check_attn(full, y=y)
