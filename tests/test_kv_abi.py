@@ -89,7 +89,7 @@ def test_attn_refusals(q):
     for n in names:
         assert call(**{n: None}) == q.QNT_ERR_ARG, n
         assert call(**{n: A + (2 if n in four else 8)}) == q.QNT_ERR_ALIGN, n
-    for kw in ({"heads": 0}, {"heads": 5}, {"heads": 65538}, {"q_stride": 248}, {"q_stride": 260}, {"y_stride": 248}, {"y_stride": 260}, {"rows": 0},
+    for kw in ({"heads": 0}, {"heads": 5}, {"tokens": q.QNT_KV_MAX_TOKENS}, {"heads": 65538}, {"q_stride": 248}, {"q_stride": 260}, {"y_stride": 248}, {"y_stride": 260}, {"rows": 0},
                {"rows": q.QNT_KV_MAX_ROWS + 1}, {"width": 0}, {"width": (1 << 26) + 1}, {"tokens": -1}, {"tokens": q.QNT_KV_MAX_TOKENS + 1}):
         assert call(**kw) == q.QNT_ERR_SHAPE, kw
     for kw in ({"max_new": 0}, {"window": -1}, {"scale": float("nan")}, {"scale": float("inf")}, {"xdtype": 7}):
