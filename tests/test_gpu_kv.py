@@ -596,3 +596,36 @@ def test_attn_window_needs_no_page_before_it():
         assert c["status"] == 0
         full = dict(c, table=np.where(c["table"] < 0, 0, c["table"]))
         check_attn(full, y=y)
+
+
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+@pytest.mark.parametrize("new", [1, 40])
+def test_cache_beyond_32_bit_offsets(fmt, new):
+    """Codes of 5.2 GB: pages at both ends, written by an append and read by attention."""
+    Q = H.q()
+    page, heads, dim, pages = 128, 8, 128, 40000
+    d = Q.kv_desc(fmt, page, pages, heads, dim)
+    assert Q.qnt_kv_codes_bytes(d) > 2 ** 32
+    codes = [torch.empty(Q.qnt_kv_codes_bytes(d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = torch.zeros(2, pages, heads, device="cuda")
+    ids, L, tokens = [39998, 5, 39999], 300, 300
+    slot = np.array([ids[t // page] * page + t % page for t in range(L)])
+    x = values(3, tokens, heads * dim, 0)
+    st = dev([0])
+    Q.qnt_kv_append(d, codes[0], codes[1], scales[0], scales[1], x[0].cuda(), x[1].cuda(), heads * dim, dev(slot), tokens, 0, st)
+    q = torch.randn(new, 2 * heads * dim, generator=torch.Generator().manual_seed(1)).half()
+    y = torch.zeros(new, 2 * heads * dim, dtype=torch.float16, device="cuda")
+    work = H.dev_bytes(Q.qnt_kv_attn_work_bytes(d, 2 * heads, new))
+    Q.qnt_kv_attn(d, codes[0], codes[1], scales[0], scales[1], q.cuda(), 2 * heads * dim, y, 2 * heads * dim, 2 * heads, dev([0, new]), dev([L]), dev([ids]),
+                  1, 3, new, new, 0.09, 0, work, 0, st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    c = [k.view(pages, heads, page, dim)[ids].cpu().numpy() for k in codes]
+    s = [k[ids].cpu().numpy() for k in scales]
+    small = np.array([t for t in range(L)])
+    for i in range(2):
+        want_c, want_s, _ = R.append(fmt, page, c[i], np.zeros((3, heads), np.float32), x[i].double().numpy().reshape(tokens, heads, dim), small)
+        assert np.array_equal(s[i], want_s) and np.array_equal(c[i][:2], want_c[:2]) and np.array_equal(c[i][2, :, :L - 256], want_c[2, :, :L - 256])
+    want, bound = R.attn(fmt, page, c[0], c[1], s[0], s[1], q.double().numpy().reshape(new, 2 * heads, dim), np.array([0, new]), np.array([L]),
+                         np.array([[0, 1, 2]]), 0.09, 0, torch.finfo(torch.float16).eps)
+    assert (np.abs(y.double().cpu().numpy().reshape(want.shape) - want) <= bound).all()
