@@ -91,7 +91,8 @@ __device__ __forceinline__ void decode_v(uint32_t s, uint32_t t, uint32_t (&o)[4
 
 // What a request asks of the kernel.
 struct KaRow {
-  int first, n, len, begin;    // first token row, new tokens, cached tokens, first token of the work
+  int first, n, len;           // first token row, new tokens, cached tokens
+  int seen, begin;             // first token that a row sees, first token of the work
   int tiles;                   // groups of query rows
   int units;                   // units of one (head, group)
   long long all;
@@ -102,7 +103,8 @@ __device__ __forceinline__ KaRow ka_row(const KvAttnArgs& A, int b) {
   w.first = min(max(A.cu[b], 0), A.tokens);
   w.n = min(max(A.cu[b + 1], w.first), A.tokens) - w.first;
   w.len = min(max(A.len[b], 0), A.width << A.page_log2);
-  w.begin = A.window ? max(w.len - w.n + 1 - A.window, 0) & ~15 : 0;   // no page before the window is looked up
+  w.seen = A.window ? max(w.len - w.n + 1 - A.window, 0) : 0;
+  w.begin = w.seen & ~15;      // no page before the window is looked up
   w.tiles = (int)(((long long)w.n * A.group + ROWS - 1) / ROWS);
   w.units = max(1, (w.len - w.begin + UNIT - 1) / UNIT);
   w.all = (long long)w.n * A.group > A.narrow ? 0 : (long long)w.tiles * w.units * A.heads;
@@ -422,14 +424,16 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
           p[nb][nr][0] = transpose8x8(pack_f16(e[0], e[1]));
           p[nb][nr][1] = transpose8x8(pack_f16(e[2], e[3]));
         }
-      if (FMT == QNT_KV_E4M3 && tk + TT > w.len) {           // bytes behind the last token may be NaN
+      if (FMT == QNT_KV_E4M3 && (tk + TT > w.len || tk < w.seen)) {   // bytes that no row sees may be NaN
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (tk + 16 * nb + 2 * r + (i & 1) + 8 * (i >> 1) >= w.len)
+          for (int i = 0; i < 4; ++i) {
+            const int j = tk + 16 * nb + 2 * r + (i & 1) + 8 * (i >> 1);
+            if (j >= w.len || j < w.seen)
 #pragma unroll
               for (int k = 0; k < VW; ++k) vreg[nb][i][k] = 0;
+          }
       }
       const uint32_t one = 0x3C003C00u;
 #pragma unroll

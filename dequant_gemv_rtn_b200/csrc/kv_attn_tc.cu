@@ -76,7 +76,7 @@ template <int D> struct Kt {
 };
 
 struct KtRow { int first, n, len, rows, tiles; long long all, per_head; };
-struct KtTile { int t_first, t_last, begin, end, units; };
+struct KtTile { int t_first, t_last, seen, begin, end, units; };   // seen: the first token that a row sees
 
 // Tokens that the rows [row0, row0 + cap) of a request see.
 __device__ __forceinline__ KtTile kt_tile(const KvAttnArgs& A, const KtRow& w, int row0, int cap) {
@@ -84,7 +84,8 @@ __device__ __forceinline__ KtTile kt_tile(const KvAttnArgs& A, const KtRow& w, i
   t.t_first = token_of(A, row0);
   t.t_last = token_of(A, min(w.rows, row0 + cap) - 1);
   const int base = w.len - w.n;
-  t.begin = A.window ? max(base + t.t_first + 1 - A.window, 0) & ~15 : 0;
+  t.seen = A.window ? max(base + t.t_first + 1 - A.window, 0) : 0;
+  t.begin = t.seen & ~15;
   t.end = min(w.len, base + t.t_last + 1);
   t.units = max(1, (t.end - t.begin + kKtTok - 1) / kKtTok);
   return t;
@@ -728,15 +729,15 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
     float2 sc = make_float2(0.0f, 0.0f);                      // first warp: scales of the tile's runs of 16 tokens
     uint32_t it = 0;
     bool ok = true;
-    auto load_pages = [&](const int32_t* table, int h, int tok0, int end) {
+    auto load_pages = [&](const int32_t* table, int h, int tok0, int seen, int end) {
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         const int tok = tok0 + my_tok + TPI * i;
-        page[i] = tok < end ? table[tok >> pl] : -1;
+        page[i] = tok < end && tok >= seen ? table[tok >> pl] : -1;   // what no row sees may be NaN: not read
       }
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
-        if (tok0 + my_tok + TPI * i < end && (unsigned)page[i] >= (unsigned)A.pages) page[i] = 0;
+        if (tok0 + my_tok + TPI * i < end && tok0 + my_tok + TPI * i >= seen && (unsigned)page[i] >= (unsigned)A.pages) page[i] = 0;
       if (dw == 0) {
         const int tok = tok0 + 16 * lane;
         sc = make_float2(0.0f, 0.0f);
@@ -773,8 +774,8 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       const int ntiles = job.u1 - job.u0;
       const int32_t* const table = A.table + (size_t)slot.walk.b * A.width;
       int tok0 = job.t.begin + job.u0 * kKtTok;
-      const int end_tok = job.t.end, h = job.h;
-      load_pages(table, h, tok0, end_tok);
+      const int end_tok = job.t.end, seen_tok = job.t.seen, h = job.h;
+      load_pages(table, h, tok0, seen_tok, end_tok);
       load(A.kcodes, h, tok0, kreg);
       load(A.vcodes, h, tok0, vreg);
       for (int i = 0; i < ntiles; ++i, ++it, tok0 += kKtTok) {
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
 #endif
           if (lane == 0 && !skip) mbar_arrive(k_full + stage);
           if (i + 1 < ntiles) {
-            load_pages(table, h, tok0 + kKtTok, end_tok);
+            load_pages(table, h, tok0 + kKtTok, seen_tok, end_tok);
             load(A.kcodes, h, tok0 + kKtTok, kreg);
           }
         }

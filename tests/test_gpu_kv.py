@@ -629,3 +629,14 @@ def test_cache_beyond_32_bit_offsets(fmt, new):
     want, bound = R.attn(fmt, page, c[0], c[1], s[0], s[1], q.double().numpy().reshape(new, 2 * heads, dim), np.array([0, new]), np.array([L]),
                          np.array([[0, 1, 2]]), 0.09, 0, torch.finfo(torch.float16).eps)
     assert (np.abs(y.double().cpu().numpy().reshape(want.shape) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 128)])
+@pytest.mark.parametrize("new", [1, 2, 70])
+def test_attn_bytes_before_the_window_may_be_nan(dim, page, new):
+    """The window begins inside a page: what is before it there, seen by no query, does not reach the result."""
+    c = make_attn(dim + new, R.E4M3, 0, page, 1, 4, dim, [700, 357], [new, 1], window=99)
+    for b in range(2):
+        first = max(0, int(c["lens"][b]) - int(c["cu"][b + 1] - c["cu"][b]) + 1 - 99)
+        c["codes"][:, c["table"][b, first // page], :, :first % page] = 0x7F
+    check_attn(c)
