@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
     // the run is refused if its page had one before it with only skipped rows in between
     const int prev = start > 0 ? slot_s[start - 1] : -1;
     const bool first = live && (idx == start || tid == 0);
-    bool refuse = first && prev >= 0 && (prev >> pl) == (s >> pl);
-    uint32_t look = __ballot_sync(0xffffffffu, first && prev < 0);
+    bool refuse = first && prev >= 0 && prev != kApBad && (prev >> pl) == (s >> pl);
+    uint32_t look = __ballot_sync(0xffffffffu, first && (prev < 0 || prev == kApBad));
     while (look) {
       const int src = __ffs(look) - 1;
       look &= look - 1;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
 #pragma unroll
         for (int i = 7; i >= 0; --i) {         // rows at - 255 .. at, the nearest counts
           const int r = at - 32 * i - lane;
-          if (r >= 0 && A.slots[r] >= 0) near = 32 * i + lane;
+          if (r >= 0 && (unsigned)A.slots[r] < (unsigned)limit) near = 32 * i + lane;
         }
         near = __reduce_min_sync(0xffffffffu, near);
         if (near < 256) found = A.slots[at - near];

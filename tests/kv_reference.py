@@ -98,7 +98,7 @@ def append(fmt, page, codes, scales, x, slot):
     while t < n:
         s = int(slot[t])
         if s >= pages * page:
-            status, t, last = ARG, t + 1, s
+            status, t = ARG, t + 1
             continue
         if s < 0:
             t += 1

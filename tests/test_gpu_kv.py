@@ -640,3 +640,23 @@ def test_attn_bytes_before_the_window_may_be_nan(dim, page, new):
         first = max(0, int(c["lens"][b]) - int(c["cu"][b + 1] - c["cu"][b]) + 1 - 99)
         c["codes"][:, c["table"][b, first // page], :, :first % page] = 0x7F
     check_attn(c)
+
+
+def test_append_second_run_behind_a_bad_slot_is_refused():
+    """A slot beyond the cache is a skipped row, also between two runs of a page."""
+    Q = H.q()
+    page, heads, dim, pages = 16, 2, 64, 3
+    d = Q.kv_desc(R.INT8, page, pages, heads, dim)
+    slot = np.array([16, 17, pages * page + 4, -1, 20, 21, 32, 33])
+    x = values(11, len(slot), heads * dim, 0)
+    codes = [dev(np.full((pages, heads, page, dim), 200), torch.uint8) for _ in range(2)]
+    scales = torch.zeros(2, pages, heads, device="cuda")
+    st = dev([0])
+    Q.qnt_kv_append(d, codes[0], codes[1], scales[0], scales[1], x[0].cuda(), x[1].cuda(), heads * dim, dev(slot), len(slot), 0, st)
+    torch.cuda.synchronize()
+    assert int(st) == R.ARG
+    for i in range(2):
+        want_c, want_s, status = R.append(R.INT8, page, np.full((pages, heads, page, dim), 200, np.uint8), np.zeros((pages, heads), np.float32),
+                                          x[i].double().numpy().reshape(-1, heads, dim), slot)
+        assert status == R.ARG
+        assert np.array_equal(codes[i].cpu().numpy(), want_c) and np.array_equal(scales[i].cpu().numpy(), want_s)
