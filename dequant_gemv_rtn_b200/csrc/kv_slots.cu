@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kSlThreads) kv_slots_kernel(const KvSlotsArgs 
       if (fits && (need == 0 || need_end[r] <= have)) {
         const int p = len + (t - first), used = (len + P - 1) / P, j = p / P;
         const int page = j < used ? A.table[(size_t)r * A.width + j] : stack(have - 1 - (need0 + j - used));
-        slot = page * P + (p - j * P);
+        // a page outside the cache: a slot outside it, too, not one that the product wraps to
+        slot = (unsigned)page < (unsigned)A.pages ? page * P + (p - j * P) : 0x7FFFFFFF;
       }
     }
     A.slots[t] = slot;

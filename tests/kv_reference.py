@@ -82,7 +82,8 @@ def slots(page, pages, length, add, table, free, count, tokens):
         len_out[b] = length[b] + n
         for t in range(n):
             p = int(length[b]) + t
-            out[begin + t] = int(table[b, p // page]) * page + p % page
+            pg = int(table[b, p // page])
+            out[begin + t] = pg * page + p % page if 0 <= pg < pages else 2 ** 31 - 1
     left = len(stack)
     if left > count:
         free[count:left] = stack[count:]

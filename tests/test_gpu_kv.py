@@ -660,3 +660,22 @@ def test_append_second_run_behind_a_bad_slot_is_refused():
                                           x[i].double().numpy().reshape(-1, heads, dim), slot)
         assert status == R.ARG
         assert np.array_equal(codes[i].cpu().numpy(), want_c) and np.array_equal(scales[i].cpu().numpy(), want_s)
+
+
+def test_slots_of_pages_outside_the_cache():
+    """Their tokens get a slot that qnt_kv_append refuses, whatever the product with the page size would wrap to."""
+    Q = H.q()
+    page, pages, rows, width, tokens = 16, 40, 4, 5, 12
+    length, add = np.array([18, 3, 16, 16]), np.array([2, 1, 2, 3])
+    table = np.zeros((rows, width), np.int64)
+    table[0, :2], table[1, 0], table[2, 0], table[3, 0] = [4, 1 << 28], -1, 5, 6
+    free = np.zeros(pages, np.int64)
+    free[:3] = [7, (1 << 28) + 1, 9]
+    d = Q.kv_desc(R.INT8, page, pages, 1, 64)
+    t, f, out, cu, slot, count, st = dev(table), dev(free), dev(np.zeros(rows)), dev(np.zeros(rows + 1)), dev(np.zeros(tokens)), dev([0]), dev([0])
+    Q.qnt_kv_slots(d, dev(length), dev(add), t, f, dev([3]), out, cu, slot, count, rows, width, tokens, st)
+    torch.cuda.synchronize()
+    none = 2 ** 31 - 1
+    assert slot.tolist() == [none, none, none, 9 * page, 9 * page + 1, none, none, none] + [-1] * 4
+    assert [int(x) for x in R.slots(page, pages, length, add, table, free, 3, tokens)[4]] == slot.tolist()
+    assert t[2, 1] == 9 and t[3, 1] == (1 << 28) + 1 and int(count) == 1
