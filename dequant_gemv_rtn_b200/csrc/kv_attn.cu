@@ -115,7 +115,7 @@ template <int FMT, bool BF16, int D, int NR, int W, int PER_SM>
 __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArgs A) {
   constexpr int kKaWarps = W, kKaThreads = 32 * W;
   constexpr int ROWS = 8 * NR;                              // query rows of a CTA
-  constexpr int TT = (D == 256 || NR > 1) ? 16 : 32;        // tokens of a warp's step
+  constexpr int TT = D == 256 ? 16 : 32;                    // tokens of a warp's step
   constexpr int NB = TT / 16;
   constexpr int UNIT = kKaWarps * TT;
   constexpr int C = D / 64;                                 // 16-byte pieces of a K token that a lane holds
@@ -593,7 +593,11 @@ cudaError_t ka_launch_w(const KvAttnArgs& a, cudaStream_t s) {
 }
 template <int FMT, bool BF16, int D, int NR>
 cudaError_t ka_launch(const KvAttnArgs& a, long long rows, cudaStream_t s) {
-  constexpr int PER_SM = D == 64 && NR == 1 ? 4 : D == 256 ? 2 : 3;
+  // 16 query rows of 128: two CTAs leave registers for steps of 32 tokens a warp, whose
+  // loads are what keeps memory busy (64 rows of 16 query heads a head to 16384 tokens:
+  // 252 us; three CTAs and steps of 16: 274; two and 16: 296).  24 rows a pass in two
+  // CTAs' registers were slower than 16 in two passes (28 drafted rows, 8 heads: 76, 65).
+  constexpr int PER_SM = D == 64 && NR == 1 ? 4 : D == 256 || (D == 128 && NR > 1) ? 2 : 3;
   static_assert(PER_SM <= kKaMaxPerSm, "workspace");
   // A few long jobs are cut into many parts each; one large CTA per SM then leaves a
   // third of the parts to merge (one row of 131072 tokens on 8 heads: 60 -> 53 us),
