@@ -622,8 +622,8 @@ cudaError_t ka_dim(int dim, const KvAttnArgs& a, long long rows, cudaStream_t s)
 // more go to kv_attn_tc.cu's.  16 rows a pass cost a pass over the tokens each, the
 // tcgen05 kernel costs the same up to 256 rows, but its few large jobs take longer to
 // start and to merge.  So the border goes by the number of jobs (us here / there, 6500
-// tokens, 8 heads): 2 requests of 48 rows 33 / 42, 96 rows 47 / 52, 128 rows 57 / 55;
-// 16 requests of 48 rows 162 / 141, 64 rows 207 / 142, 96 rows 305 / 148; 16 requests
+// tokens, 8 heads): 2 requests of 48 rows 29 / 42, 96 rows 40 / 52, 128 rows 50 / 53;
+// 16 requests of 48 rows 141 / 145, 64 rows 182 / 147, 96 rows 267 / 152; 16 requests
 // of 35 rows on 4 heads, 3000 tokens, 58 / 60.
 constexpr int kKaNarrow = 32, kKaNarrowFewJobs = 96;
 int ka_narrow(const KvAttnArgs& a) { return a.rows * a.heads >= 128 ? kKaNarrow : kKaNarrowFewJobs; }
