@@ -94,7 +94,8 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
 // The same with t = x * inv next to a tie somewhere: the sign of a remainder,
 // rounded once, decides.  INT8: x - q s against s / 2 (exact: q s has 31 bits, the
 // difference cancels to 24).  E4M3: t is moved off the five-bit number m that it
-// is next to, to the side that x - m s tells.
+// is next to, to the side that x - m s tells (away from 0 if that has t's sign; by sign
+// bits, since t may have underflowed to a zero).
 template <int FMT, bool BF16>
 __device__ __forceinline__ uint2 codes_near(uint4 v, float s, float inv) {
   if (FMT == QNT_KV_E4M3 && s == 0.0f) return make_uint2(0, 0);
@@ -116,7 +117,7 @@ __device__ __forceinline__ uint2 codes_near(uint4 v, float s, float inv) {
     } else {
       const uint32_t b = __float_as_uint(t), m = (b + 4u) & ~0x7FFFFu;
       const float r = fmaf(-__uint_as_float(m), s, x);
-      const uint32_t to = r == 0.0f ? m : (r > 0.0f) == (t > 0.0f) ? m + 1u : m - 1u;
+      const uint32_t to = r == 0.0f ? m : (r < 0.0f) == ((int)b < 0) ? m + 1u : m - 1u;
       c[j] = ((b + 4u) & 0x7FFFFu) < 9u ? to : b;
     }
   }
