@@ -29,7 +29,11 @@
 //    2^4 and 2^-6: beyond that u moves and O is rescaled, as for the maximum.  So
 //    a weight keeps its fp16 precision unless its page's scale is below 2^-8 or so
 //    of that of another in the same 128 tokens; then its absolute error is 2^-25
-//    of the larger scale.
+//    of the larger scale.  Two limits keep both factors in fp32's range, since scales
+//    may differ by 2^270: a page's values do not count below 2^-40 of u (2^(u - log2
+//    vs) would overflow, and its weights vanish from the sum), and u does not fall below
+//    2^-64 of the highest it had (O, whose weights of then may be all that counts,
+//    would overflow).
 //  * Work is cut into equal parts of tiles of all requests, one per CTA, as in
 //    kv_attn.cu, here with each row tile's own causal range.
 //
@@ -59,6 +63,9 @@ constexpr int kKtGroups = kKtTok / 16;       // runs of 16 tokens: one page each
 constexpr int kKtCtrl = 5120;                // barriers, scales, the warps' jobs
 constexpr int kKtScaleRing = 4;
 constexpr int kKtSlots = 2048;               // where the warps' jobs begin
+// log2 of V scales: below the unit by more than kKtNone a page's values do not count;
+// the unit stays within kKtFall of the highest it had.
+constexpr float kKtNone = 40.0f, kKtFall = 64.0f;
 constexpr uint32_t kKtCols = 512;
 constexpr unsigned long long kKtTimeoutNs = 2000000000ull;
 
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       const bool on = kKtRows * s < job.rows;                 // the stream has rows
       alone = job.rows <= kKtRows;
       const int t = token_of(A, row), hq = job.h * A.group + row - t * A.group;
-      float m = kKaFloor, l = 0.0f, unit = 0.0f;
+      float m = kKaFloor, l = 0.0f, unit = 0.0f, highest = 0.0f;
       bool has_unit = false, ok = true;
       if (on) {
         // Q in fp16, bf16 rows scaled by a power of two; a negative factor goes into Q
@@ -473,11 +480,13 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           const float lv = sc[kKtGroups].y;
           if (lv > -INFINITY) {
             if (!has_unit) {
-              unit = lv;
+              unit = highest = lv;
               has_unit = true;
             } else if (lv - unit > 4.0f || lv - unit < -6.0f) {
-              grow = exp2_approx(unit - lv);
-              unit = lv;
+              highest = fmaxf(highest, lv);
+              const float next = fmaxf(lv, highest - kKtFall);
+              grow = exp2_approx(unit - next);
+              unit = next;
             }
           }
           auto hide = [&](uint32_t (&v)[32], int q) {          // what the row does not see becomes -infinity
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
               for (int h2 = 0; h2 < 2; ++h2) {
                 const float2 f = *reinterpret_cast<const float2*>(sc + 2 * q + h2);
                 const float c = factor(c0, f.x);
-                const bool none = f.y == -INFINITY;           // V's scale is 0: the weights count, the values do not
+                const bool none = f.y < unit - kKtNone;       // V's scale is 0, or nearly: the weights count, the values do not
                 const float ref = none ? m : m - (f.y - unit);
                 const uint64_t c2 = pair_f32(c, c), ref2 = pair_f32(-ref, -ref);
                 float e[16];

@@ -1,4 +1,8 @@
-"""The key/value cache calls where magnitudes lie far apart or at the ends of their types."""
+"""The key/value cache calls where the magnitudes lie far apart or at the ends of their types, for both attention kernels:
+scales from the subnormals to the top of bf16, zero scales, long tails of the softmax.  The 64-bit result and the bound
+are computed here, per token, so that one page's size does not loosen the bound of another's."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +11,77 @@ from tests import kv_reference as R
 from tests import test_gpu_kv as T
 
 pytestmark = pytest.mark.gpu
+
+WIDE = 128      # query rows of a key/value head that go to the tcgen05 kernel whatever the number of jobs
+
+
+def exact(c, requests):
+    """(y, bound) [tokens][heads][dim] in 64 bits, NaN in rows of no request.  How far a kernel may be off:
+    - logits: fp32 sums of products of up to 255 (INT8's offset codes, its 128 taken off: 383) or 448 times the scale, 16
+      roundings of 2^-24, and 4 of the logit itself: a weight's relative error 2 dx;
+    - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of the reference's and of
+      2^7 times the largest V scale of the same 128 tokens (here: within 128 on either side); the weights of a page whose
+      V scale is 2^-40 of that or less count, its values do not;
+    - sums: a rounding of what is summed up per 16 tokens, which is the weighted |values| and, for INT8 in the mma.sync
+      kernel, 128 scales a weight more that are taken off again;
+    - the type's half step (of its subnormals: eps / 2 of the smallest normal number), and 2^-96."""
+    fmt, page, D = c["fmt"], c["page"], c["dim"]
+    top = 383.0 if fmt == R.INT8 else 448.0
+    table = torch.from_numpy(R.value(np.arange(256), fmt)).cuda()
+    codes = [torch.from_numpy(k).cuda() for k in c["codes"]]
+    scales = torch.from_numpy(c["scales"]).cuda().double()
+    kv, group = c["kv_heads"], c["heads"] // c["kv_heads"]
+    q = c["q"].cuda().double()
+    y = torch.full(q.shape, math.nan, dtype=torch.float64, device="cuda")
+    bound = y.clone()
+    eps, least = torch.finfo(T.TYPES[c["xdt"]]).eps, torch.finfo(T.TYPES[c["xdt"]]).smallest_normal
+    for b in requests:
+        L, n, first = int(c["lens"][b]), int(c["cu"][b + 1] - c["cu"][b]), int(c["cu"][b])
+        ids = torch.from_numpy(np.asarray(c["table"][b, :-(-L // page)])).cuda().long()
+        for h in range(kv):
+            k, v = [(table[x[ids, h].long()] * scales[i, ids, h][:, None, None]).reshape(-1, D)[:L] for i, x in enumerate(codes)]
+            ks, vs = [scales[i, ids, h].repeat_interleave(page)[:L] for i in (0, 1)]
+            near = torch.nn.functional.max_pool1d(vs[None, None], 257, 1, 128)[0, 0]
+            for t in range(n):
+                p = L - n + t
+                lo = max(0, p - c["window"] + 1) if c["window"] else 0
+                rows = q[first + t, h * group:(h + 1) * group]
+                x = rows @ k[lo:p + 1].T * c["scale"]
+                w = torch.exp(x - x.amax(1, keepdim=True))
+                w = w / w.sum(1, keepdim=True)
+                peak = w.amax(1, keepdim=True)                     # 1 / the sum of weights relative to the reference
+                r = w @ v[lo:p + 1]
+                vv, sv, nv = v[lo:p + 1].abs(), vs[lo:p + 1], near[lo:p + 1]
+                size = w @ vv
+                dx = 2.0 ** -20 * top * abs(c["scale"]) * rows.abs().sum(1, keepdim=True) * ks[lo:p + 1].max() + 2.0 ** -22 * x.abs().amax(1, keepdim=True)
+                steps = (p + 1 - lo) / 16 + 16
+                summed = size if fmt == R.E4M3 or n * group >= WIDE else size + 256 * (w @ sv)[:, None]
+                cut = (2.0 ** -18 * (nv * top).sum() * peak + 2.0 ** -33 * (w @ (nv * top))[:, None] + (p + 1 - lo) * 2.0 ** -25 * peak * r.abs())
+                bound[first + t, h * group:(h + 1) * group] = ((2.0 ** -11 + 2 * dx) * (size + r.abs()) + cut + steps * 2.0 ** -23 * summed
+                                                               + eps / 2 * (r.abs() * 1.01 + least) + 2.0 ** -96)
+                y[first + t, h * group:(h + 1) * group] = r
+    return y, bound
+
+
+def copies(c, times):
+    """The same requests `times` over, on the same pages: jobs enough that a CTA goes through several tiles of one."""
+    n = int(c["cu"][-1])
+    return dict(c, lens=np.tile(c["lens"], times), table=np.tile(c["table"], (times, 1)), q=c["q"][:n].repeat(times, 1, 1), tokens=n * times,
+                cu=np.concatenate([c["cu"][:-1] + n * t for t in range(times)] + [[n * times]]), times=times)
+
+
+def check(c):
+    y = T.call_attn(c)
+    assert c["status"] == 0
+    times = c.get("times", 1)
+    want, bound = exact(c, range(len(c["lens"]) // times))
+    part = len(want) // times
+    want, bound = (x[:part].repeat(times, 1, 1) if times > 1 else x for x in (want, bound))
+    live = ~want.isnan()
+    err = (y.double() - want).abs()
+    bad = ~(err <= bound) & live
+    assert not bad.any(), (int(bad.sum()), float((err / bound)[live].max()), y[bad][:3], want[bad][:3], bad.nonzero()[:3])
+    return y
 
 
 # ------------------------------------------------------------------ append
@@ -23,3 +98,43 @@ def test_append_quotients_that_underflow(fmt, top):
         x[0, t, 20 + t:27 + t], x[1, t, 20 + t:27 + t] = -tiny, tiny
     codes, scales = T.make_cache(9, fmt, 2, heads, page, dim)
     T.check_append(fmt, 1, page, dim, heads, codes, scales, x.bfloat16(), np.arange(5))
+
+
+# ------------------------------------------------------------------ V scales
+def far_apart(kind, fmt, xdt, dim, page, group, new, lens=(700, 333)):
+    c = T.make_attn(dim + page + group, fmt, xdt, page, 1, group, dim, list(lens), [new] * len(lens), nan_behind=False)
+    r = np.random.default_rng(len(kind))
+    tb, s = c["table"], c["scales"]
+    tiles = max(1, 128 // page)                                    # pages of 128 tokens
+    if kind == "decades":
+        s[1] *= (10.0 ** r.integers(-8, 4, s[1].shape)).astype(np.float32)
+        s[:, tb[0, 1]] = 0
+    elif kind == "one page":
+        for b in range(len(lens)):
+            s[1, tb[b, 1]] = [1e-40, 1e-43, 1e-38, 0.0][b % 4]
+    elif kind == "subnormal tile":
+        s[1, tb[0, tiles:2 * tiles]] = 1e-40
+        s[1, tb[1, :tiles]] = 1e-44
+    elif kind == "zero tiles":
+        s[1, tb[0, :tiles]] = 0
+        s[1, tb[0, 2 * tiles:3 * tiles]] = 0
+        s[1, tb[1, tiles:2 * tiles]] = 0
+    elif kind == "up and down":
+        f = (10.0 ** np.array([0, 12, -12, 25, -25, 3, -30, 30, -3, 0, 1, -1])).astype(np.float32)
+        for b in range(len(lens)):
+            for j in range(-(-lens[b] // page)):
+                s[1, tb[b, j]] = 1e-2 * f[(j // tiles) % len(f)]
+    elif kind == "all tiny":
+        s[1] *= np.float32(1e-36)
+    elif kind == "bits":
+        s[1] = (2.0 ** r.uniform(-150, 3, s[1].shape)).astype(np.float32)
+    return c
+
+
+@pytest.mark.parametrize("kind", ["decades", "one page", "subnormal tile", "zero tiles", "up and down", "all tiny", "bits"])
+@pytest.mark.parametrize("fmt,xdt,dim,page", [(R.INT8, 1, 128, 64), (R.E4M3, 0, 64, 16), (R.E4M3, 1, 256, 32), (R.INT8, 0, 64, 128)])
+@pytest.mark.parametrize("group,new", [(4, 40), (2, 1)])
+def test_attn_v_scales_far_apart(kind, fmt, xdt, dim, page, group, new):
+    c = far_apart(kind, fmt, 1 if kind in ("all tiny", "up and down") else xdt, dim, page, group, new)
+    check(c)
+    check(copies(c, 150))
