@@ -20,20 +20,21 @@
 //    first softmax warp issues its MMAs, which has nothing else to do by then.
 //  * Four warps per stream do the softmax, a thread a row, 32 columns at a time in
 //    two loops (the maximum; the weights), packed fp32 arithmetic taking two logits
-//    at once.  Only if one passes the reference by 8 (2^8: fp16 takes it) is the
-//    reference moved and O rescaled before its next product.
+//    at once.  Only if one passes the reference by 8 is the reference moved and O
+//    rescaled before its next product.
 //  * Scales: K's multiplies the row's factor, per 16 tokens (a page or a part of
 //    one).  V's goes into the exponent: the weight that meets V's codes is
 //    2^(x - m + log2(vs) - u), and a page's share of the sum is taken back by
 //    2^(u - log2 vs) once per 16 tokens.  u is the largest V scale of the tile, within
-//    2^4 and 2^-6: beyond that u moves and O is rescaled, as for the maximum.  So
-//    a weight keeps its fp16 precision unless its page's scale is below 2^-8 or so
-//    of that of another in the same 128 tokens; then its absolute error is 2^-25
-//    of the larger scale.  Two limits keep both factors in fp32's range, since scales
-//    may differ by 2^270: a page's values do not count below 2^-40 of u (2^(u - log2
-//    vs) would overflow, and its weights vanish from the sum), and u does not fall below
-//    2^-64 of the highest it had (O, whose weights of then may be all that counts,
-//    would overflow).
+//    a factor of two: beyond that u moves and O is rescaled, as for the maximum.
+//    With the 2^6 that every weight carries (what the slack of the reference and of u
+//    leaves of fp16's range; it cancels with the sum) a weight has fp16's 11 bits down
+//    to 2^-20 of the reference and u, and below that an absolute error of 2^-31 of
+//    them, 2^-30 of the tile's largest scale.
+//    Two limits keep both factors in fp32's range, since scales may differ by 2^270:
+//    a page's values do not count below 2^-40 of u (2^(u - log2 vs) would overflow, and
+//    its weights vanish from the sum), and u does not fall below 2^-64 of the highest
+//    it had (O, whose weights of then may be all that counts, would overflow).
 //  * Work is cut into equal parts of tiles of all requests, one per CTA, as in
 //    kv_attn.cu, here with each row tile's own causal range.
 //
@@ -63,6 +64,10 @@ constexpr int kKtGroups = kKtTok / 16;       // runs of 16 tokens: one page each
 constexpr int kKtCtrl = 5120;                // barriers, scales, the warps' jobs
 constexpr int kKtScaleRing = 4;
 constexpr int kKtSlots = 2048;               // where the warps' jobs begin
+// A weight at the reference is held as 2^kKtBias; a new reference is at most kKaSlack
+// behind the maximum, and the unit at most kKtNear behind a tile's: 2^15 in all, which fp16 takes.
+constexpr float kKtBias = 6.0f, kKtNear = 1.0f;
+static_assert(kKtBias + kKaSlack + kKtNear <= 15.0f, "weights in fp16");
 // log2 of V scales: below the unit by more than kKtNone a page's values do not count;
 // the unit stays within kKtFall of the highest it had.
 constexpr float kKtNone = 40.0f, kKtFall = 64.0f;
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
             if (!has_unit) {
               unit = highest = lv;
               has_unit = true;
-            } else if (lv - unit > 4.0f || lv - unit < -6.0f) {
+            } else if (fabsf(lv - unit) > kKtNear) {
               highest = fmaxf(highest, lv);
               const float next = fmaxf(lv, highest - kKtFall);
               grow = exp2_approx(unit - next);
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
               if (k > hi_k || k <= lo_k) v[k] = 0xFF800000u;
           };
           // the tile's maximum, 32 columns at a time, before the stream's turn
-          float top = m;
+          float top = -INFINITY;
 #pragma unroll 1
           for (int q2 = 0; q2 < kKtTok / 32; q2 += 2) {
 #pragma unroll
@@ -518,9 +523,10 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           }
           tmem_ld32(ts, x[0]);
           float alpha = 1.0f;
-          if (__any_sync(0xffffffffu, top > m + kKaSlack)) {
-            alpha = exp2_approx(m - top);
-            m = top;
+          if (__any_sync(0xffffffffu, top > m + (kKaSlack + kKtBias))) {
+            const float next = fmaxf(m, top - kKtBias);       // m: the reference, less the bias
+            alpha = exp2_approx(m - next);
+            m = next;
           }
           // the weights; P's columns 16 q .. 16 q + 15 lie in S's that are read already
           turn_wait();

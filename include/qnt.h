@@ -413,10 +413,10 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  * power of two per row where it is bf16), the softmax is fp32, its weights are
  * rounded to fp16 for the second product, relative to a running maximum, and y
  * once to its type.  (Requests of more than 32 query rows a key/value head may go to
- * the tcgen05 tensor cores.  There a weight also carries its page's V scale: in
- * pages whose V scale is less than 2^-8 of another's in the same 128 tokens its
- * absolute error is 2^-25 of the larger, and below 2^-40 of it their values count as
- * 0, their weights in full.)  The bytes of tokens that no query sees
+ * the tcgen05 tensor cores.  There a weight also carries its page's V scale: its
+ * relative error is 2^-11 or its absolute error 2^-30 of the largest weight and of the
+ * largest V scale of the 128 tokens around it, and in pages below 2^-40 of that scale
+ * the values count as 0, their weights in full.)  The bytes of tokens that no query sees
  * may be anything; a visible E4M3 byte must not be 0x7F or 0xFF (NaN;
  * qnt_kv_append writes none).
  * A page number outside the cache is read as page 0, and d_len beyond

@@ -19,9 +19,10 @@ def exact(c, requests):
     """(y, bound) [tokens][heads][dim] in 64 bits, NaN in rows of no request.  How far a kernel may be off:
     - logits: fp32 sums of products of up to 255 (INT8's offset codes, its 128 taken off: 383) or 448 times the scale, 16
       roundings of 2^-24, and 4 of the logit itself: a weight's relative error 2 dx;
-    - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of the reference's and of
-      2^7 times the largest V scale of the same 128 tokens (here: within 128 on either side); the weights of a page whose
-      V scale is 2^-40 of that or less count, its values do not;
+    - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of what holds them: the
+      reference's, in numerator and sum, for the mma.sync kernel; for the tcgen05 kernel, in the numerator, 2^-6 of the
+      reference's and twice the largest V scale of the same 128 tokens (here: within 128 on either side), and the values of
+      pages whose V scale is 2^-40 of that or less count as 0;
     - sums: a rounding of what is summed up per 16 tokens, which is the weighted |values| and, for INT8 in the mma.sync
       kernel, 128 scales a weight more that are taken off again;
     - the type's half step (of its subnormals: eps / 2 of the smallest normal number), and 2^-96."""
@@ -49,14 +50,17 @@ def exact(c, requests):
                 x = rows @ k[lo:p + 1].T * c["scale"]
                 w = torch.exp(x - x.amax(1, keepdim=True))
                 w = w / w.sum(1, keepdim=True)
-                peak = w.amax(1, keepdim=True)                     # 1 / the sum of weights relative to the reference
+                peak = w.amax(1, keepdim=True)                     # 1 / the sum of weights relative to the largest
                 r = w @ v[lo:p + 1]
                 vv, sv, nv = v[lo:p + 1].abs(), vs[lo:p + 1], near[lo:p + 1]
                 size = w @ vv
                 dx = 2.0 ** -20 * top * abs(c["scale"]) * rows.abs().sum(1, keepdim=True) * ks[lo:p + 1].max() + 2.0 ** -22 * x.abs().amax(1, keepdim=True)
                 steps = (p + 1 - lo) / 16 + 16
                 summed = size if fmt == R.E4M3 or n * group >= WIDE else size + 256 * (w @ sv)[:, None]
-                cut = (2.0 ** -18 * (nv * top).sum() * peak + 2.0 ** -33 * (w @ (nv * top))[:, None] + (p + 1 - lo) * 2.0 ** -25 * peak * r.abs())
+                if n * group >= WIDE:
+                    cut = 2.0 ** -30 * R.TOP[fmt] * nv.sum() * peak + 2.0 ** -39 * R.TOP[fmt] * (w @ nv)[:, None]
+                else:
+                    cut = 2.0 ** -25 * peak * (vv.sum(0) + (p + 1 - lo) * r.abs())
                 bound[first + t, h * group:(h + 1) * group] = ((2.0 ** -11 + 2 * dx) * (size + r.abs()) + cut + steps * 2.0 ** -23 * summed
                                                                + eps / 2 * (r.abs() * 1.01 + least) + 2.0 ** -96)
                 y[first + t, h * group:(h + 1) * group] = r
@@ -138,3 +142,24 @@ def test_attn_v_scales_far_apart(kind, fmt, xdt, dim, page, group, new):
     c = far_apart(kind, fmt, 1 if kind in ("all tiny", "up and down") else xdt, dim, page, group, new)
     check(c)
     check(copies(c, 150))
+
+
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+def test_attn_long_tail_behind_a_page_of_large_values(fmt):
+    """Tokens of 2^-20 of the largest weight each, 65536 of them: a sixteenth of the largest weight together.  The first page's V scale is
+    60 times the others'.  148 requests over the same pages keep a job whole."""
+    L, page, dim, group = 65536, 64, 64, WIDE
+    pages = L // page
+    codes = np.full((2, pages, 1, page, dim), 128 if fmt == R.INT8 else 0, np.uint8)
+    r = np.random.default_rng(5)
+    codes[0, 0, 0, 3, 0] = 255 if fmt == R.INT8 else 0x7E          # the token that takes most
+    big = r.integers(60, 100, (pages, page, dim))
+    codes[1, :, 0] = R.nearest(big.astype(np.float64) * (1 if fmt == R.INT8 else 3), fmt)
+    codes[1, 0, 0] = R.nearest(r.integers(-2, 3, (page, dim)).astype(np.float64), fmt)
+    scales = np.full((2, pages, 1), 1 / R.TOP[fmt], np.float32)
+    scales[1, 0] *= 60
+    q = torch.zeros(1, group, dim)
+    q[:, :, 0] = 20 * math.log(2) * 8
+    c = dict(fmt=fmt, xdt=0, page=page, pages=pages, width=pages, kv_heads=1, heads=group, dim=dim, lens=np.array([L]), cu=np.array([0, 1]),
+             table=np.arange(pages)[None], codes=codes, scales=scales, q=q.half(), tokens=1, window=0, scale=0.125, max_new=1)
+    check(copies(c, 148))
