@@ -26,7 +26,9 @@
 //    page's scale, however small or large, costs no precision.
 //  * p is rounded to fp16 for the second product (relative error 2^-11, which
 //    averages out over tokens; the sum uses the rounded values).  m follows the
-//    maximum only when a logit passes it by 8 (p <= 2^8), decided by one vote.
+//    maximum only when a logit passes it by 8, decided by one vote.  Every p carries
+//    2^7, what that leaves of fp16's range (it cancels with the sum): full precision
+//    down to 2^-21 of the reference, below that an absolute error of 2^-32 of it.
 //  * Work: units of 16 or 32 tokens a warp of one (request, key/value head, group of
 //    query rows), in one row of all units of the call, cut into equal parts,
 //    one per CTA.  So requests of very unlike length keep every SM busy, and
@@ -48,6 +50,9 @@ namespace {
 
 constexpr int kKaBatch = 10;                      // parts of a split job that a thread reads at once
 constexpr int kKaMaxPerSm = 4;                    // CTAs per SM of any variant
+// A weight at the reference is held as 2^kKaBias; with the slack of the reference 2^15 in all.
+constexpr float kKaBias = 7.0f;
+static_assert(kKaBias + kKaSlack <= 15.0f, "weights in fp16");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -390,16 +395,17 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int k = 0; k < 4; ++k) over = fmaxf(over, s[nb][nr][k] - m[nr][k & 1]);
-      if (__any_sync(0xffffffffu, over > kKaSlack)) {
+      if (__any_sync(0xffffffffu, over > kKaSlack + kKaBias)) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = m[nr][i];
+            float top = -INFINITY;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) top = fmaxf(top, fmaxf(s[nb][nr][i], s[nb][nr][i + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(m[nr][i], top - kKaBias);            // m: the reference, less the bias
             const float alpha = exp2_approx(m[nr][i] - top);
             m[nr][i] = top;
             corr[nr][i] *= alpha;

@@ -411,14 +411,14 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  *              enough for.  Two calls that may run at the same time need two.
  * Products are of exact fp16 operands with fp32 accumulation (q is rescaled by a
  * power of two per row where it is bf16), the softmax is fp32, its weights are
- * rounded to fp16 for the second product, relative to a running maximum, and y
- * once to its type.  (Requests of more than 32 query rows a key/value head may go to
- * the tcgen05 tensor cores.  There a weight also carries its page's V scale: its
- * relative error is 2^-11 or its absolute error 2^-30 of the largest weight and of the
- * largest V scale of the 128 tokens around it, and in pages below 2^-40 of that scale
- * the values count as 0, their weights in full.)  The bytes of tokens that no query sees
- * may be anything; a visible E4M3 byte must not be 0x7F or 0xFF (NaN;
- * qnt_kv_append writes none).
+ * rounded to fp16 for the second product (relative error 2^-11 or absolute error
+ * 2^-32 of the largest), and y once to its type.  (Requests of more than 32 query
+ * rows a key/value head may go to the tcgen05 tensor cores.  There a weight also
+ * carries its page's V scale: its relative error is 2^-11 or its absolute error 2^-30
+ * of the largest weight and of the largest V scale of the 128 tokens around it, and in
+ * pages below 2^-40 of that scale the values count as 0, their weights in full.)
+ * The bytes of tokens that no query sees may be anything; a visible E4M3 byte must
+ * not be 0x7F or 0xFF (NaN; qnt_kv_append writes none).
  * A page number outside the cache is read as page 0, and d_len beyond
  * width * page is cut there (QNT_ERR_ARG in *d_status).
  */

@@ -19,8 +19,8 @@ def exact(c, requests):
     """(y, bound) [tokens][heads][dim] in 64 bits, NaN in rows of no request.  How far a kernel may be off:
     - logits: fp32 sums of products of up to 255 (INT8's offset codes, its 128 taken off: 383) or 448 times the scale, 16
       roundings of 2^-24, and 4 of the logit itself: a weight's relative error 2 dx;
-    - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of what holds them: the
-      reference's, in numerator and sum, for the mma.sync kernel; for the tcgen05 kernel, in the numerator, 2^-6 of the
+    - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of what holds them: 2^-7 of
+      the reference's, in numerator and sum, for the mma.sync kernel; for the tcgen05 kernel, in the numerator, 2^-6 of the
       reference's and twice the largest V scale of the same 128 tokens (here: within 128 on either side), and the values of
       pages whose V scale is 2^-40 of that or less count as 0;
     - sums: a rounding of what is summed up per 16 tokens, which is the weighted |values| and, for INT8 in the mma.sync
@@ -60,7 +60,7 @@ def exact(c, requests):
                 if n * group >= WIDE:
                     cut = 2.0 ** -30 * R.TOP[fmt] * nv.sum() * peak + 2.0 ** -39 * R.TOP[fmt] * (w @ nv)[:, None]
                 else:
-                    cut = 2.0 ** -25 * peak * (vv.sum(0) + (p + 1 - lo) * r.abs())
+                    cut = 2.0 ** -32 * peak * (vv.sum(0) + (p + 1 - lo) * r.abs())
                 bound[first + t, h * group:(h + 1) * group] = ((2.0 ** -11 + 2 * dx) * (size + r.abs()) + cut + steps * 2.0 ** -23 * summed
                                                                + eps / 2 * (r.abs() * 1.01 + least) + 2.0 ** -96)
                 y[first + t, h * group:(h + 1) * group] = r
@@ -163,3 +163,22 @@ def test_attn_long_tail_behind_a_page_of_large_values(fmt):
     c = dict(fmt=fmt, xdt=0, page=page, pages=pages, width=pages, kv_heads=1, heads=group, dim=dim, lens=np.array([L]), cu=np.array([0, 1]),
              table=np.arange(pages)[None], codes=codes, scales=scales, q=q.half(), tokens=1, window=0, scale=0.125, max_new=1)
     check(copies(c, 148))
+
+
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+def test_attn_long_tail_of_single_tokens(fmt):
+    """Tokens of 2^-25.5 of the largest weight each, 262144 of them: half a percent of the sum.  600 requests over the same
+    pages keep a job whole."""
+    L, page, dim, group = 262144, 128, 64, 8
+    pages = L // page
+    codes = np.full((2, pages, 1, page, dim), 128 if fmt == R.INT8 else 0, np.uint8)
+    codes[0, 0, 0, 3, 0] = 255 if fmt == R.INT8 else 0x7E
+    codes[1] = 228 if fmt == R.INT8 else R.nearest(np.array([300.0]), fmt)[0]
+    codes[1, 0] = codes[0, 1, 0, 0, 1]                             # zero
+    scales = np.full((2, pages, 1), 1 / R.TOP[fmt], np.float32)
+    q = torch.zeros(1, group, dim)
+    q[:, :, 0] = 25.5 * math.log(2) * 8
+    q[:, 1:, 1:] = 1e-3 * torch.randn(group - 1, dim - 1, generator=torch.Generator().manual_seed(1))
+    c = dict(fmt=fmt, xdt=0, page=page, pages=pages, width=pages, kv_heads=1, heads=group, dim=dim, lens=np.array([L]), cu=np.array([0, 1]),
+             table=np.arange(pages)[None], codes=codes, scales=scales, q=q.half(), tokens=1, window=0, scale=0.125, max_new=1)
+    check(copies(c, 600))
