@@ -202,7 +202,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // A logit's factor; never 0, since it meets -infinity.
-__device__ __forceinline__ float factor(float row, float scale) { return fmaxf(row * scale, 1e-37f); }
+constexpr float kKtLeast = 1e-37f;
+__device__ __forceinline__ float factor(float row, float scale) { return fmaxf(row * scale, kKtLeast); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* d) {
   asm volatile(
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       alone = job.rows <= kKtRows;
       const int t = token_of(A, row), hq = job.h * A.group + row - t * A.group;
       float m = kKaFloor, l = 0.0f, unit = 0.0f, highest = 0.0f;
-      bool has_unit = false, ok = true;
+      bool has_unit = false, far = false, ok = true;
       if (on) {
         // Q in fp16, bf16 rows scaled by a power of two; a negative factor goes into Q
         const uint16_t* const src = static_cast<const uint16_t*>(A.q) + (int64_t)(slot.walk.w.first + t) * A.q_stride + (int64_t)hq * D;
@@ -527,6 +528,27 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
             const float next = fmaxf(m, top - kKtBias);       // m: the reference, less the bias
             alpha = exp2_approx(m - next);
             m = next;
+            far = __any_sync(0xffffffffu, fabsf(m) > 1048576.0f && m != kKaFloor);
+          }
+          // Beyond 2^20 a logit's product with its factor is rounded as the maximum's was before
+          // the reference is taken off (an exact product and a rounded one may differ by any
+          // number there).  S becomes that difference, apart from the loop below.
+          float row_c = c0, least_c = kKtLeast, at = m;
+          if (far) {
+#pragma unroll 1
+            for (int q = 0; q < kKtTok / 32; ++q) {
+              if (q) tmem_ld32(ts + 32u * (uint32_t)q, x[0]);
+              tmem_wait_ld32(x[0]);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                x[0][k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[0][k]), factor(c0, sc[2 * q + k / 16].x)), m));
+              tmem_st16(ts + 32u * (uint32_t)q, *reinterpret_cast<uint32_t(*)[16]>(x[0]));
+              tmem_st16(ts + 32u * (uint32_t)q + 16u, *reinterpret_cast<uint32_t(*)[16]>(x[0] + 16));
+            }
+            tmem_wait_st();
+            tmem_ld32(ts, x[0]);
+            row_c = at = 0.0f;
+            least_c = 1.0f;
           }
           // the weights; P's columns 16 q .. 16 q + 15 lie in S's that are read already
           turn_wait();
@@ -544,9 +566,9 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
                 const float2 f = *reinterpret_cast<const float2*>(sc + 2 * q + h2);
-                const float c = factor(c0, f.x);
+                const float c = fmaxf(row_c * f.x, least_c);  // factor(c0, f.x)
                 const bool none = f.y < unit - kKtNone;       // V's scale is 0, or nearly: the weights count, the values do not
-                const float ref = none ? m : m - (f.y - unit);
+                const float ref = none ? at : at - (f.y - unit);
                 const uint64_t c2 = pair_f32(c, c), ref2 = pair_f32(-ref, -ref);
                 float e[16];
 #pragma unroll

@@ -182,3 +182,28 @@ def test_attn_long_tail_of_single_tokens(fmt):
     c = dict(fmt=fmt, xdt=0, page=page, pages=pages, width=pages, kv_heads=1, heads=group, dim=dim, lens=np.array([L]), cu=np.array([0, 1]),
              table=np.arange(pages)[None], codes=codes, scales=scales, q=q.half(), tokens=1, window=0, scale=0.125, max_new=1)
     check(copies(c, 600))
+
+
+# ------------------------------------------------------------------ the ends of bf16
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+@pytest.mark.parametrize("group,new", [(4, 40), (8, 1)])
+@pytest.mark.parametrize("lens", [(300, 200), (20011, 50)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e12, 1e25])
+def test_attn_logits_of_any_size(fmt, group, new, lens, sign, size):
+    """Every logit is `size` or so, of one sign, a token's twice or half that: it takes all."""
+    page, dim = 64, 64
+    c = T.make_attn(8, fmt, 1, page, 1, group, dim, lens, [new, new], nan_behind=False)
+    code = {k: R.nearest(np.full((1,), k * R.TOP[fmt]), fmt)[0] for k in (-1.0, -0.5, 0.5, 1.0)}
+    most, rest = (1.0, 0.5) if sign > 0 else (-0.5, -1.0)
+    c["codes"][0] = code[rest]
+    c["codes"][0, c["table"][0, 2], 0, 5] = c["codes"][0, c["table"][1, 0], 0, 1] = code[most]
+    c["scales"][0] = np.float32(1e-3 / R.TOP[fmt])
+    c["q"][:] = size / 64 * 1e3 / c["scale"]
+    y = T.call_attn(c)
+    assert c["status"] == 0
+    for b, (pg, tok) in enumerate(((2, 5), (0, 1))):
+        at = c["table"][b, pg]
+        want = torch.from_numpy(R.value(c["codes"][1, at, 0, tok], fmt) * float(c["scales"][1, at, 0])).cuda()
+        got = y[int(c["cu"][b]):int(c["cu"][b + 1])].double()
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-30).all(), (got.flatten()[:4], want[:4])
