@@ -7,7 +7,7 @@
 namespace qnt {
 
 constexpr size_t kKaCounters = 16384;             // workspace: counters in front of the partial results
-constexpr float kKaFloor = -1e30f;                // reference of the softmax before the first token
+constexpr float kKaFloor = -3e38f;                // reference of the softmax before the first token, below any logit
 constexpr float kKaSlack = 8.0f;                  // log2 of the largest weight: the reference moves when one passes it
 
 __device__ __forceinline__ float exp2_approx(float x) {

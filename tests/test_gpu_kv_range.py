@@ -189,7 +189,7 @@ def test_attn_long_tail_of_single_tokens(fmt):
 @pytest.mark.parametrize("group,new", [(4, 40), (8, 1)])
 @pytest.mark.parametrize("lens", [(300, 200), (20011, 50)])
 @pytest.mark.parametrize("sign", [1, -1])
-@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e12, 1e25])
+@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e12, 1e25, 1e32])
 def test_attn_logits_of_any_size(fmt, group, new, lens, sign, size):
     """Every logit is `size` or so, of one sign, a token's twice or half that: it takes all."""
     page, dim = 64, 64
