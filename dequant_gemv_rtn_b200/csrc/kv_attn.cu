@@ -53,6 +53,9 @@ constexpr int kKaMaxPerSm = 4;                    // CTAs per SM of any variant
 // A weight at the reference is held as 2^kKaBias; with the slack of the reference 2^15 in all.
 constexpr float kKaBias = 7.0f;
 static_assert(kKaBias + kKaSlack <= 15.0f, "weights in fp16");
+// INT8 logits come in units of 2^-24.  The row's factor takes 2^16 of that and K's scale 2^8,
+// so that neither overflows where bf16 queries or keys do not.
+constexpr float kKaRowUp = 65536.0f, kKaScaleUp = 256.0f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         float up, down;
         f16_range(top, up, down);
-        factor *= down;
+        factor *= top > 0.0f ? down : 0.0f;                 // (a query of zero may meet a scale of any size)
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
           for (int i = 0; i < 8; ++i) sum += h2f(q[nr][c][i] & 0xFFFFu) + h2f(q[nr][c][i] >> 16);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        factor *= 16777216.0f;                              // codes are q 2^-24
+        factor *= kKaRowUp;                                 // codes are q 2^-24
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {                          // row n's values are in the lanes with g = n
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(32 * W, PER_SM) kv_attn_kernel(const KvAttnArg
       }
       float ks_now[NB];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) ks_now[nb] = ks[nb];
+      for (int nb = 0; nb < NB; ++nb) ks_now[nb] = FMT == QNT_KV_INT8 ? ks[nb] * kKaScaleUp : ks[nb];
       load_k(tk + UNIT);                                     // with the pages read a step ahead
       // base-2 logits, relative to the reference
       float over = 0.0f;

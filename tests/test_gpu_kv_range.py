@@ -189,7 +189,7 @@ def test_attn_long_tail_of_single_tokens(fmt):
 @pytest.mark.parametrize("group,new", [(4, 40), (8, 1)])
 @pytest.mark.parametrize("lens", [(300, 200), (20011, 50)])
 @pytest.mark.parametrize("sign", [1, -1])
-@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e12, 1e25, 1e32])
+@pytest.mark.parametrize("size", [1e6, 1e8, 1e9, 1e12, 1e25, 1e32, 1e36])
 def test_attn_logits_of_any_size(fmt, group, new, lens, sign, size):
     """Every logit is `size` or so, of one sign, a token's twice or half that: it takes all."""
     page, dim = 64, 64
@@ -207,3 +207,13 @@ def test_attn_logits_of_any_size(fmt, group, new, lens, sign, size):
         want = torch.from_numpy(R.value(c["codes"][1, at, 0, tok], fmt) * float(c["scales"][1, at, 0])).cuda()
         got = y[int(c["cu"][b]):int(c["cu"][b + 1])].double()
         assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-30).all(), (got.flatten()[:4], want[:4])
+
+
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+@pytest.mark.parametrize("group,new", [(4, 40), (8, 1)])
+def test_attn_queries_of_zero_meet_keys_of_any_size(fmt, group, new):
+    """Their logits are 0: an even mean."""
+    c = T.make_attn(7, fmt, 1, 32, 1, group, 128, [300, 200], [new, new], nan_behind=False)
+    c["scales"][0] = np.float32(1e36)
+    c["q"][:] = 0
+    check(c)
