@@ -34,7 +34,8 @@
 //    Two limits keep both factors in fp32's range, since scales may differ by 2^270:
 //    a page's values do not count below 2^-40 of u (2^(u - log2 vs) would overflow, and
 //    its weights vanish from the sum), and u does not fall below 2^-64 of the highest
-//    it had (O, whose weights of then may be all that counts, would overflow).
+//    it had (O, whose weights of then may be all that counts, would overflow) nor below
+//    2^-100 (2^u, and that over the sum of weights, would be 0).
 //  * Work is cut into equal parts of tiles of all requests, one per CTA, as in
 //    kv_attn.cu, here with each row tile's own causal range.
 //
@@ -69,8 +70,8 @@ constexpr int kKtSlots = 2048;               // where the warps' jobs begin
 constexpr float kKtBias = 6.0f, kKtNear = 1.0f;
 static_assert(kKtBias + kKaSlack + kKtNear <= 15.0f, "weights in fp16");
 // log2 of V scales: below the unit by more than kKtNone a page's values do not count;
-// the unit stays within kKtFall of the highest it had.
-constexpr float kKtNone = 40.0f, kKtFall = 64.0f;
+// the unit stays within kKtFall of the highest it had, and above kKtLowest.
+constexpr float kKtNone = 40.0f, kKtFall = 64.0f, kKtLowest = -100.0f;
 constexpr uint32_t kKtCols = 512;
 constexpr unsigned long long kKtTimeoutNs = 2000000000ull;
 
@@ -486,11 +487,11 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           const float lv = sc[kKtGroups].y;
           if (lv > -INFINITY) {
             if (!has_unit) {
-              unit = highest = lv;
+              unit = highest = fmaxf(lv, kKtLowest);
               has_unit = true;
             } else if (fabsf(lv - unit) > kKtNear) {
               highest = fmaxf(highest, lv);
-              const float next = fmaxf(lv, highest - kKtFall);
+              const float next = fmaxf(fmaxf(lv, kKtLowest), highest - kKtFall);
               grow = exp2_approx(unit - next);
               unit = next;
             }

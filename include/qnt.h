@@ -415,8 +415,11 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  * 2^-32 of the largest), and y once to its type.  (Requests of more than 32 query
  * rows a key/value head may go to the tcgen05 tensor cores.  There a weight also
  * carries its page's V scale: its relative error is 2^-11 or its absolute error 2^-30
- * of the largest weight and of the largest V scale of the 128 tokens around it, and in
- * pages below 2^-40 of that scale the values count as 0, their weights in full.)
+ * of the largest weight and of the largest V scale of the 128 tokens around it (or
+ * 2^-100), and in pages below 2^-40 of that scale the values count as 0, their weights
+ * in full.)
+ * All of that is fp32: the terms scale * q_i * k_i of a logit and the logit have to
+ * stay below 2^120 and cached values below 2^96 in magnitude.
  * The bytes of tokens that no query sees may be anything; a visible E4M3 byte must
  * not be 0x7F or 0xFF (NaN; qnt_kv_append writes none).
  * A page number outside the cache is read as page 0, and d_len beyond

@@ -21,11 +21,12 @@ def exact(c, requests):
       roundings of 2^-24, and 4 of the logit itself: a weight's relative error 2 dx;
     - weights: half a step of fp16 (2^-11 of the weight) or, where they are subnormal, 2^-25 of what holds them: 2^-7 of
       the reference's, in numerator and sum, for the mma.sync kernel; for the tcgen05 kernel, in the numerator, 2^-6 of the
-      reference's and twice the largest V scale of the same 128 tokens (here: within 128 on either side), and the values of
-      pages whose V scale is 2^-40 of that or less count as 0;
+      reference's and twice the largest V scale of the same 128 tokens (here: within 128 on either side), or of 2^-100 if
+      that is more, and the values of pages whose V scale is 2^-40 of that or less count as 0;
     - sums: a rounding of what is summed up per 16 tokens, which is the weighted |values| and, for INT8 in the mma.sync
       kernel, 128 scales a weight more that are taken off again;
-    - the type's half step (of its subnormals: eps / 2 of the smallest normal number), and 2^-96."""
+    - the type's half step (of its subnormals: eps / 2 of the smallest normal number);
+    - half a subnormal step of fp32 of each of these sums: 2^-149 a step."""
     fmt, page, D = c["fmt"], c["page"], c["dim"]
     top = 383.0 if fmt == R.INT8 else 448.0
     table = torch.from_numpy(R.value(np.arange(256), fmt)).cuda()
@@ -42,7 +43,7 @@ def exact(c, requests):
         for h in range(kv):
             k, v = [(table[x[ids, h].long()] * scales[i, ids, h][:, None, None]).reshape(-1, D)[:L] for i, x in enumerate(codes)]
             ks, vs = [scales[i, ids, h].repeat_interleave(page)[:L] for i in (0, 1)]
-            near = torch.nn.functional.max_pool1d(vs[None, None], 257, 1, 128)[0, 0]
+            near = torch.nn.functional.max_pool1d(vs[None, None], 257, 1, 128)[0, 0].clamp(min=2.0 ** -100)
             for t in range(n):
                 p = L - n + t
                 lo = max(0, p - c["window"] + 1) if c["window"] else 0
@@ -62,7 +63,7 @@ def exact(c, requests):
                 else:
                     cut = 2.0 ** -32 * peak * (vv.sum(0) + (p + 1 - lo) * r.abs())
                 bound[first + t, h * group:(h + 1) * group] = ((2.0 ** -11 + 2 * dx) * (size + r.abs()) + cut + steps * 2.0 ** -23 * summed
-                                                               + eps / 2 * (r.abs() * 1.01 + least) + 2.0 ** -96)
+                                                               + eps / 2 * (r.abs() * 1.01 + least) + 2.0 ** -149 * steps)
                 y[first + t, h * group:(h + 1) * group] = r
     return y, bound
 
@@ -216,4 +217,15 @@ def test_attn_queries_of_zero_meet_keys_of_any_size(fmt, group, new):
     c = T.make_attn(7, fmt, 1, 32, 1, group, 128, [300, 200], [new, new], nan_behind=False)
     c["scales"][0] = np.float32(1e36)
     c["q"][:] = 0
+    check(c)
+
+
+@pytest.mark.parametrize("fmt", [R.INT8, R.E4M3])
+@pytest.mark.parametrize("dim,page,lens", [(64, 16, (20011, 200)), (128, 64, (9001, 40)), (256, 32, (333, 70))])
+@pytest.mark.parametrize("group,new", [(4, 40), (8, 1)])
+@pytest.mark.parametrize("size", [7.9e28, 1e20, 1e-31, 1e-36])
+def test_attn_values_of_any_size(fmt, dim, page, lens, group, new, size):
+    """Values up to 2^96, the most that the calls take, and down to the subnormals, split jobs among them."""
+    c = T.make_attn(dim + page, fmt, 1, page, 1, group, dim, lens, [new] * len(lens), spread=0.0, nan_behind=False)
+    c["scales"][1] = np.float32(size / R.TOP[fmt])
     check(c)
