@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
             const float next = fmaxf(m, top - kKtBias);       // m: the reference, less the bias
             alpha = exp2_approx(m - next);
             m = next;
-            far = __any_sync(0xffffffffu, fabsf(m) > 1048576.0f && m != kKaFloor);
+            far = __any_sync(0xffffffffu, fabsf(m) > 1048576.0f && fabsf(m) < -kKaFloor);   // neither unset nor infinite
           }
           // Beyond 2^20 a logit's product with its factor is rounded as the maximum's was before
           // the reference is taken off (an exact product and a rounded one may differ by any
