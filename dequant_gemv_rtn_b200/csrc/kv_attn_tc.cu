@@ -409,6 +409,10 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
       free_stage(v_empty + stage);
       return true;
     };
+    auto soft_sync = [&]() {                                  // all softmax warps, each of them whole
+      __syncwarp();
+      asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+    };
     while (next_job()) {
       const int ntiles = job.u1 - job.u0;
       const int row = job.row0 + kKtRows * s + r;             // query row of the request's head
@@ -643,21 +647,23 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           uint32_t o[32];
           tmem_ld32(to + (uint32_t)c, o);
           tmem_wait_ld32(o);
-          if (!live) continue;
+          if (live) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float v[8];
+            for (int k = 0; k < 32; k += 8) {
+              float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[k + e]) * f;
-            const float4 a = make_float4(v[0], v[1], v[2], v[3]), z = make_float4(v[4], v[5], v[6], v[7]);
-            if (whole) {
-              const uint2 x = pack_out<BF16>(a), w = pack_out<BF16>(z);
-              *reinterpret_cast<uint4*>(out_at(rr) + c + k) = make_uint4(x.x, x.y, w.x, w.y);
-            } else {
-              __stcg(reinterpret_cast<float4*>(mypart + rr * D + c + k), a);
-              __stcg(reinterpret_cast<float4*>(mypart + rr * D + c + k + 4), z);
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[k + e]) * f;
+              const float4 a = make_float4(v[0], v[1], v[2], v[3]), z = make_float4(v[4], v[5], v[6], v[7]);
+              if (whole) {
+                const uint2 x = pack_out<BF16>(a), w = pack_out<BF16>(z);
+                *reinterpret_cast<uint4*>(out_at(rr) + c + k) = make_uint4(x.x, x.y, w.x, w.y);
+              } else {
+                __stcg(reinterpret_cast<float4*>(mypart + rr * D + c + k), a);
+                __stcg(reinterpret_cast<float4*>(mypart + rr * D + c + k + 4), z);
+              }
             }
           }
+          __syncwarp();                                       // the next load needs the whole warp
         }
         if (!whole && live) {
           __stcg(mypart + CAP * D + rr, m);
@@ -670,14 +676,14 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
         uint32_t* const counters = static_cast<uint32_t*>(A.work);
         const int first = parts.cta_of(job.u_first), last = parts.cta_of(job.u_first + job.t.units - 1);
         __threadfence();
-        asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+        soft_sync();
         if (tid == 0) {
           const uint32_t before = atomicAdd(counters + first, 1u);
           *last_s = before == (uint32_t)(last - first);
           if (*last_s) counters[first] = 0;                   // ready for the next call
           __threadfence();
         }
-        asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+        soft_sync();
         if (*last_s) {
           auto at = [&](int c) { return partials + (size_t)(2 * c + (c == first ? 1 : 0)) * PART; };
           constexpr int TH = 32 * T::SoftWarps;                 // a thread per row
@@ -712,13 +718,13 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           constexpr int U = 8;                                  // pieces of four values that a thread has in flight
           for (int c0 = 0; c0 < n; c0 += FIT) {                 // (one round, unless there are more parts)
             const int cn = min(FIT, n - c0);
-            if (c0) asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+            if (c0) soft_sync();
             if (mine_row)
               for (int c = 0; c < cn; ++c) {
                 const float pm = c0 ? __ldcg(at(first + c0 + c) + CAP * D + tid) : f_s[c * CAP + tid];
                 f_s[c * CAP + tid] = exp2_approx(pm - top) * inv;
               }
-            asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");
+            soft_sync();
             for (int x0 = tid; x0 < job.rows * (D / 4); x0 += U * TH) {
               float4 v[U];
 #pragma unroll
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
               }
             }
           }
-          asm volatile("bar.sync 1, %0;" :: "r"(32 * T::SoftWarps) : "memory");   // last_s is read
+          soft_sync();   // last_s is read
         }
       }
     }
