@@ -325,7 +325,7 @@ int qnt_kv_attn(const qnt_kv_desc* desc, const void* d_kcodes, const void* d_vco
   if (xdtype != QNT_F16 && xdtype != QNT_BF16) return QNT_ERR_ARG;
   if (heads < 1 || heads > 65536 || heads % desc->heads != 0) return QNT_ERR_SHAPE;
   if ((int64_t)tokens * (heads / desc->heads) > QNT_KV_MAX_TOKENS) return QNT_ERR_SHAPE;   // query rows are ints
-  if (max_new < 1 || window < 0 || !(scale > -INFINITY && scale < INFINITY)) return QNT_ERR_ARG;
+  if (max_new < 1 || window < 0 || !(std::fabs(scale) <= 18446744073709551616.0f)) return QNT_ERR_ARG;
   const int64_t row = (int64_t)heads * desc->dim;
   if ((e = check_stride(q_stride, row)) != QNT_OK || (e = check_stride(y_stride, row)) != QNT_OK) return e;
   if (tokens == 0) return QNT_OK;

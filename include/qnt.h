@@ -405,6 +405,7 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  *   d_table    device int32 [rows][width].
  *   max_new    the largest n as far as the caller knows it (>= 1): it chooses the
  *              kernel, not what is computed.
+ *   scale      at most 2^64 in magnitude.   window  0: none.
  *   d_work     device, qnt_kv_attn_work_bytes bytes for these heads and max_new,
  *              16-byte aligned, zeroed by the caller before its first use; every
  *              call leaves it ready for the next, of whatever sizes it is large

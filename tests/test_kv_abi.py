@@ -97,6 +97,17 @@ def test_attn_refusals(q):
     assert call(tokens=0) == q.QNT_OK
 
 
+def test_attn_refuses_scales_that_overflow_the_logits_factor(q):
+    d = q.kv_desc(q.QNT_KV_INT8, 16, 3, 2, 64)
+
+    def call(scale):
+        return q.qnt_kv_attn(d, A, A, A, A, A, 256, A, 256, 4, A, A, A, 2, 2, 0, 1, scale, 0, A, check=False, stream=0)
+
+    for scale in (3e38, -3e38, 2.0 ** 65, float("-inf")):
+        assert call(scale) == q.QNT_ERR_ARG, scale
+    assert call(2.0 ** 64) == q.QNT_OK and call(-(2.0 ** 64)) == q.QNT_OK     # no tokens: nothing launched
+
+
 # ------------------------------------------------------------------ the reference itself
 def test_reference_e4m3_rounding_against_torch():
     import torch
