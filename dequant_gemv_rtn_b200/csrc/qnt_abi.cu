@@ -311,7 +311,7 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
 }
 
 size_t qnt_kv_attn_work_bytes(const qnt_kv_desc* desc, int heads, int max_new) {
-  if (check_kv(desc) != QNT_OK || heads < 1 || heads % desc->heads != 0 || max_new < 1) return 0;
+  if (check_kv(desc) != QNT_OK || heads < 1 || heads > 65536 || heads % desc->heads != 0 || max_new < 1) return 0;
   return qnt::kv_attn_work_bytes(*desc, heads, max_new);
 }
 

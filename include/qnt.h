@@ -397,8 +397,8 @@ int qnt_kv_append(const qnt_kv_desc* desc, void* d_kcodes, void* d_vcodes, float
  *              q_stride elements apart (a multiple of 8, >= heads * dim).
  *   d_y        device, the same with y_stride, written in the same type for the
  *              token rows of requests; other rows are left as they are.
- *   heads      query heads, a multiple of desc->heads; tokens * heads / desc->heads
- *              at most QNT_KV_MAX_TOKENS.
+ *   heads      query heads, a multiple of desc->heads, at most 65536; tokens * heads /
+ *              desc->heads at most QNT_KV_MAX_TOKENS.
  *   d_cu       device int32 [rows + 1] as from qnt_kv_slots.
  *   d_len      device int32 [rows], cached tokens with the new ones among them
  *              (qnt_kv_slots' d_len_out).

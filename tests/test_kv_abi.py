@@ -38,6 +38,11 @@ def test_work_bytes(q):
     assert q.qnt_kv_attn_work_bytes(d, 5, 1) == 0 and q.qnt_kv_attn_work_bytes(d, 0, 1) == 0 and q.qnt_kv_attn_work_bytes(d, 4, 0) == 0
 
 
+def test_work_bytes_refuses_the_heads_that_the_call_refuses(q):
+    d = q.kv_desc(q.QNT_KV_INT8, 16, 3, 2, 64)
+    assert q.qnt_kv_attn_work_bytes(d, 65536, 1) > 0 and q.qnt_kv_attn_work_bytes(d, 65538, 1) == 0
+
+
 def test_slots_refusals(q):
     d = q.kv_desc(q.QNT_KV_INT8, 16, 3, 2, 64)
     names = ["length", "add", "table", "free", "free_count", "len_out", "cu", "slots", "free_count_out"]
