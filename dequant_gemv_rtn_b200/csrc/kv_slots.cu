@@ -145,7 +145,9 @@ __global__ void __launch_bounds__(kSlThreads) kv_slots_kernel(const KvSlotsArgs 
   }
   if (top) atomicMax(&top_s, top);
   __syncthreads();
-  const int taken = top_s, left = have - taken;
+  // (more pages released than there are: what does not fit is dropped)
+  const int taken = top_s, left = min(have - taken, A.pages);
+  bad |= have - taken > A.pages;
   if (blockIdx.x == 0) {
     if (short_of) report(A.status, QNT_ERR_PAGES);
     if (bad) report(A.status, QNT_ERR_ARG);
@@ -175,10 +177,7 @@ __global__ void __launch_bounds__(kSlThreads) kv_slots_kernel(const KvSlotsArgs 
     const int used = (A.len[r] + P - 1) / P;
     A.table[(size_t)r * A.width + used + (g - (r ? need_end[r - 1] : 0))] = stack(have - 1 - g);
   }
-  for (long long j = (long long)count + t0; j < left; j += step) {   // pushes that stay on the stack
-    if (j < A.pages) A.free[j] = stack((int)j);
-    else report(A.status, QNT_ERR_ARG);                // more pages released than there are
-  }
+  for (long long j = (long long)count + t0; j < left; j += step) A.free[j] = stack((int)j);   // pushes that stay
   const int total = min(add_end[A.rows - 1], A.tokens);
   for (int t = t0; t < A.tokens; t += step) {
     int slot = -1;

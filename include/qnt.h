@@ -352,7 +352,8 @@ int qnt_check_kv_desc(const qnt_kv_desc* desc);
  * they would pass width * page tokens or their token rows `tokens`, or when
  * d_len is outside 0..width * page (QNT_ERR_ARG in *d_status).  A page number
  * outside the cache is handed on as it is, and its tokens get the slot 2^31 - 1,
- * which qnt_kv_append refuses.  d_add below -1 is taken as -1 (QNT_ERR_ARG).
+ * which qnt_kv_append refuses.  d_add below -1 is taken as -1 (QNT_ERR_ARG).  If more
+ * pages are released than the cache has, the stack ends full (QNT_ERR_ARG).
  * 1 <= rows <= QNT_KV_MAX_ROWS, 1 <= width, width * page and tokens at most
  * QNT_KV_MAX_TOKENS, else QNT_ERR_SHAPE (here and below).
  */

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import gpu_helpers as H
 from tests import kv_reference as R
 from tests import test_gpu_kv as T
 
@@ -229,3 +230,19 @@ def test_attn_values_of_any_size(fmt, dim, page, lens, group, new, size):
     c = T.make_attn(dim + page, fmt, 1, page, 1, group, dim, lens, [new] * len(lens), spread=0.0, nan_behind=False)
     c["scales"][1] = np.float32(size / R.TOP[fmt])
     check(c)
+
+
+# ------------------------------------------------------------------ slots
+@pytest.mark.parametrize("width,length", [(4, 64), (1 << 14, 1 << 18)])
+def test_slots_more_pages_released_than_there_are(width, length):
+    """Every request claims the same pages: the stack ends full, nothing is written behind it, and the call is not held up."""
+    Q = H.q()
+    page, pages, rows = 16, 5, 64
+    d = Q.kv_desc(R.INT8, page, pages, 1, 64)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").remainder(pages).repeat(rows, 1)
+    free = T.dev(np.full(pages + 3, 77))
+    ln, cu, sl, left, st = T.dev(np.zeros(rows)), T.dev(np.zeros(rows + 1)), T.dev([7]), T.dev([0]), T.dev([0])
+    Q.qnt_kv_slots(d, T.dev(np.full(rows, length)), T.dev(np.full(rows, -1)), table, free, T.dev([0]), ln, cu, sl, left, rows, width, 1, st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.QNT_ERR_ARG and int(left) == pages and ln.tolist() == [0] * rows and sl.tolist() == [-1]
+    assert free.tolist() == [j % width % pages for j in range(pages)] + [77] * 3
