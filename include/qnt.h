@@ -354,6 +354,10 @@ int qnt_check_kv_desc(const qnt_kv_desc* desc);
  * outside the cache is handed on as it is, and its tokens get the slot 2^31 - 1,
  * which qnt_kv_append refuses.  d_add below -1 is taken as -1 (QNT_ERR_ARG).  If more
  * pages are released than the cache has, the stack ends full (QNT_ERR_ARG).
+ * The pages of a request are the first ceil(d_len / page) entries of its row, no
+ * others.  A caller that lowers d_len between two calls (drafted tokens that were
+ * refused) and thereby leaves a page behind the end puts it back itself: its entry
+ * goes to d_free[*d_free_count], and *d_free_count up by one, before the next call.
  * 1 <= rows <= QNT_KV_MAX_ROWS, 1 <= width, width * page and tokens at most
  * QNT_KV_MAX_TOKENS, else QNT_ERR_SHAPE (here and below).
  */
