@@ -100,11 +100,12 @@ def _ptr(t):
 
 
 def _current_stream() -> int:
-    """torch's current stream.  Once CUDA is up its number is asked for directly: building the Stream object costs 3 us,
-    more than a launch."""
+    """torch's current stream.  Once CUDA is up its number is asked for directly, where torch offers that: building the
+    Stream object costs 3 us, more than a launch."""
     import torch
-    if torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw and device and torch.cuda.is_initialized():
+        return raw(device())
     return torch.cuda.current_stream().cuda_stream
 
 

@@ -113,6 +113,20 @@ def test_attn_refuses_scales_that_overflow_the_logits_factor(q):
     assert call(2.0 ** 64) == q.QNT_OK and call(-(2.0 ** 64)) == q.QNT_OK     # no tokens: nothing launched
 
 
+def test_current_stream_without_the_raw_number(q, monkeypatch):
+    """A torch that does not offer the stream's number: the Stream object is asked."""
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    assert q._current_stream() == 1003
+    monkeypatch.delattr(torch._C, "_cuda_getDevice")
+    assert q._current_stream() == 77
+
+
 # ------------------------------------------------------------------ the reference itself
 def test_reference_e4m3_rounding_against_torch():
     import torch
