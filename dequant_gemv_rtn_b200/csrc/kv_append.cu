@@ -28,8 +28,10 @@
 // page of seven a is a multiple of 7, and then 2 % of all x / s are ties: with the
 // 64-bit quotient for these, too, 8192 prompt tokens took 52 us.)
 //
-// Bound by memory for prompts (2 bytes read and 1 written per value), by latency
-// for a decode step.
+// Prompts are bound by instructions (11 a value, 57 % of the issue slots) and the five
+// barriers of a window, not by memory: 8192 rows of 8 heads of 128 take 23.7 us for
+// 50 MB (2 bytes read and 1 written per value), a third of the copy rate.  A decode
+// step (64 rows: 3.0 us) is bound by latency, two waits for memory.
 #include "common.cuh"
 #include "kernels.h"
 

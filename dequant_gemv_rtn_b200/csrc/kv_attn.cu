@@ -38,8 +38,8 @@
 //    last (one counter), in CTA order, so the result does not depend on timing.
 //
 // Measured (B200): 64 requests of 8192 tokens on 8 heads of 128 (64 query heads),
-// E4M3: 178 us, 6.06 TB/s; lengths from 1 to 16384: 190 us, 5.7 TB/s; one request of
-// 131072, INT8: 52 us, 5.1 TB/s.  One of 700 tokens on 32 heads: 8.4 us, of which 1.4
+// E4M3: 178 us, 6.06 TB/s; lengths from 1 to 16384: 190 to 196 us, 5.6 TB/s; one request
+// of 131072, INT8: 53 us, 5.1 TB/s.  One of 700 tokens on 32 heads: 8.4 us, of which 1.4
 // is the schedule, 3 until the first bytes are there, 1 the tokens, 2.5 publishing
 // and merging six parts a head.
 #include <climits>
@@ -633,7 +633,9 @@ cudaError_t ka_dim(int dim, const KvAttnArgs& a, long long rows, cudaStream_t s)
 // start and to merge.  So the border goes by the number of jobs (us here / there, 6500
 // tokens, 8 heads): 2 requests of 48 rows 29 / 42, 96 rows 40 / 52, 128 rows 50 / 53;
 // 16 requests of 48 rows 141 / 145, 64 rows 182 / 147, 96 rows 267 / 152; 16 requests
-// of 35 rows on 4 heads, 3000 tokens, 58 / 60.
+// of 35 rows on 4 heads, 3000 tokens, 58 / 60.  Those are all at dim 128; between 16
+// and 128 jobs nothing was measured, and at dim 256, whose passes are of 8 rows, 16
+// requests of 24 rows take 224 / 213, so the border is too high there.
 constexpr int kKaNarrow = 32, kKaNarrowFewJobs = 96;
 int ka_narrow(const KvAttnArgs& a) { return a.rows * a.heads >= 128 ? kKaNarrow : kKaNarrowFewJobs; }
 

@@ -21,7 +21,8 @@
 //  * Four warps per stream do the softmax, a thread a row, 32 columns at a time in
 //    two loops (the maximum; the weights), packed fp32 arithmetic taking two logits
 //    at once.  Only if one passes the reference by 8 is the reference moved and O
-//    rescaled before its next product.
+//    rescaled before its next product.  Logits beyond 2^20 take a loop more (with the
+//    choice inside the loop of the weights every call was 6 % slower).
 //  * Scales: K's multiplies the row's factor, per 16 tokens (a page or a part of
 //    one).  V's goes into the exponent: the weight that meets V's codes is
 //    2^(x - m + log2(vs) - u), and a page's share of the sum is taken back by
@@ -40,9 +41,10 @@
 //    kv_attn.cu, here with each row tile's own causal range.
 //
 // Measured on two chunks of 1024 tokens, the cache 5000 and 8000 long (32 / 8 heads,
-// dim 128, INT8): 297 us, 676 TFLOP/s (the mma.sync kernel: 1268 us).  A tile takes
-// 5100 cycles, of which a stream's maximum 800, its weights 2200 (the other stream's
-// turn meanwhile is over or not begun) and its two products 1500.  Slower were, in
+// dim 128, INT8): 301 us, 668 TFLOP/s (the mma.sync kernel: 1268 us); 297 without the
+// limits on the unit and the way of large logits.  Then a tile took 5100 cycles, of
+// which a stream's maximum 800, its weights 2200 (the other stream's turn meanwhile is
+// over or not begun) and its two products 1500.  Slower were, in
 // us: the loops over a tile's columns unrolled, with the row in registers (437 to
 // 570: instruction fetch), one pass with the weights corrected where the maximum
 // moved (359), no turns (371 against 343 then), two threads a row (400 and, with
