@@ -757,6 +757,10 @@ __global__ void __launch_bounds__(Kt<D>::Threads, 1) kv_attn_tc_kernel(const KvA
           }
           soft_sync();   // last_s is read
         }
+      } else if (NS == 2 && alone) {
+        // the stream without rows skipped the job's tiles: it may go on when the other has
+        // taken them, since a wait by parity tells a stage's use only from the one before
+        soft_sync();
       }
     }
     if (issuing && elect_one()) tc_commit(drained);           // arrives once every MMA issued has completed

@@ -10,6 +10,7 @@ import torch
 from tests import gpu_helpers as H
 from tests import kv_reference as R
 from tests import test_gpu_kv as T
+from tests import test_gpu_kv_range as G
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,13 @@ def test_calls_repeat_bit_for_bit():
                 a @ a
         for i, c in enumerate(cases):
             assert torch.equal(T.call_attn(c, work=work[k % 2]), first[i])
+
+
+@pytest.mark.parametrize("fmt,xdt,dim,page,kv_heads,group,new,lens,window", [
+    (R.INT8, 1, 64, 32, 2, 64, 22, [169], 0), (R.E4M3, 1, 64, 64, 1, 64, 26, [276, 271], 129), (R.E4M3, 0, 128, 16, 1, 7, 44, [271, 273], 0),
+    (R.INT8, 0, 128, 64, 1, 7, 42, [166, 177], 0), (R.INT8, 1, 64, 16, 1, 7, 40, [70, 157], 500), (R.INT8, 0, 64, 64, 1, 130, 10, [15, 744, 2102, 612], 500),
+    (R.E4M3, 1, 128, 128, 1, 1, 300, [900, 1300], 0)])
+def test_jobs_of_one_tile_of_rows_beside_jobs_of_two(fmt, xdt, dim, page, kv_heads, group, new, lens, window):
+    """A CTA's next job has rows for both streams after one that had rows for the first only (up to 128 rows over a multiple of 256)."""
+    assert 0 < new * group % 256 <= 128
+    G.check(G.copies(T.make_attn(dim + group, fmt, xdt, page, kv_heads, group, dim, lens, [new] * len(lens), window=window), 150))
